@@ -379,6 +379,120 @@ NERF_API nerf_status nerf_hash_encode_backward(const float* x, int64_t n, const 
                                                float* grad_table, int deterministic,
                                                void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixtures of experts: the KiloNeRF router's general form (points sent to any
+ * number of experts each, with weights, and back), its gradients, the per-cell
+ * networks on the sorted rows with their weight gradient, and the distillation
+ * loss that teaches a gate. The KiloNeRF page (abstract) describes the grid of
+ * tiny networks and names distillation as the way to train them; the shapes are
+ * this library's.
+ *
+ * A point's j-th pair p = point * k + j goes to expert ids[point][j]; an id
+ * outside 0..n_experts-1 (-1 by convention) drops the pair. Rows are dense
+ * [rows][width] of `dtype`; weights, losses, weight gradients and every sum are
+ * fp32. Buffers of one call must not overlap. n >= 1, 1 <= k <= 64,
+ * n * k <= 2^30, 1 <= n_experts <= 4096, 1 <= width <= 2^20, pointers aligned
+ * to their element; rows that start on 16-byte boundaries move fastest.
+ * Common errors: NERF_ERR_INVALID_ARG, NERF_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+enum { NERF_DTYPE_FP32 = 0, NERF_DTYPE_BF16 = 1, NERF_DTYPE_FP16 = 2 };
+
+/* Bytes of workspace that nerf_expert_sort needs for these sizes (host). */
+NERF_API nerf_status nerf_expert_sort_workspace(int64_t n, int k, int n_experts,
+                                                int64_t* out_bytes);
+
+/* Stable counting sort of the kept pairs by expert: ids [n][k] int32;
+ * out_offset [n_experts + 1] int32: the first sorted row of every expert
+ * (out_offset[n_experts] = kept pairs); out_order int32 (may be NULL): the pair
+ * of every sorted row, ascending inside an expert, the entries behind the last
+ * left as they were (n * k entries at most); out_pos [n][k] int32: the sorted
+ * row of every pair, -1 for a dropped one. The result does not vary between
+ * runs. workspace: device, 16-byte aligned, workspace_bytes >= the size above,
+ * not shared with work that can overlap this call. */
+NERF_API nerf_status nerf_expert_sort(const int32_t* ids, int64_t n, int k, int n_experts,
+                                      int32_t* out_offset, int32_t* out_order, int32_t* out_pos,
+                                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/* rows[pos[i][j]] = weights[i][j] * x[i] for every kept pair (weights NULL: 1):
+ * x [n][width], pos [n][k] as nerf_expert_sort writes it (no row twice; a pair
+ * whose pos is outside 0..n*k-1 is dropped), rows [n * k][width], of which rows
+ * that no pair names are left as they were. */
+NERF_API nerf_status nerf_expert_dispatch(const void* x, int dtype, int64_t n, int width,
+                                          const int32_t* pos, int k, const float* weights,
+                                          void* rows, void* stream);
+
+/* Gradients of nerf_expert_dispatch from d_rows [n * k][width]:
+ * d_x[i] = sum_j weights[i][j] d_rows[pos[i][j]] (summed in fp32 in the order
+ * of j; 0 for a point whose pairs are all dropped) and, unless d_weights is
+ * NULL, d_weights[i][j] = <x[i], d_rows[pos[i][j]]> (0 for a dropped pair). x
+ * is read only for d_weights and may be NULL without it; d_x may be NULL with
+ * d_weights given. */
+NERF_API nerf_status nerf_expert_dispatch_backward(const void* d_rows, const void* x, int dtype,
+                                                   int64_t n, int width, const int32_t* pos, int k,
+                                                   const float* weights, void* d_x,
+                                                   float* d_weights, void* stream);
+
+/* out[i] = sum_j weights[i][j] rows[pos[i][j]] over the kept pairs (weights
+ * NULL: 1), in fp32 in the order of j, rounded once; 0 for a point whose pairs
+ * are all dropped. rows [n * k][width], out [n][width]. */
+NERF_API nerf_status nerf_expert_combine(const void* rows, int dtype, int64_t n, int width,
+                                         const int32_t* pos, int k, const float* weights,
+                                         void* out, void* stream);
+
+/* Gradients of nerf_expert_combine from d_out [n][width]:
+ * d_rows[pos[i][j]] = weights[i][j] d_out[i] (rows that no pair names are left
+ * as they were) and, unless d_weights is NULL, d_weights[i][j] =
+ * <d_out[i], rows[pos[i][j]]> (0 for a dropped pair). rows is read only for
+ * d_weights and may be NULL without it; d_rows may be NULL with d_weights given. */
+NERF_API nerf_status nerf_expert_combine_backward(const void* d_out, const void* rows, int dtype,
+                                                  int64_t n, int width, const int32_t* pos, int k,
+                                                  const float* weights, void* d_rows,
+                                                  float* d_weights, void* stream);
+
+/* Distillation of a gate (or of any distribution over n_classes) from the k
+ * logits that a teacher kept of each row: with q = softmax(student / T) over
+ * all classes and p = softmax(teacher / T) over the row's kept entries,
+ *   out_loss[i] = T^2 sum_j p_j (log p_j - log q[ids[i][j]])
+ *   out_grad[i] = d (row_scale[i] out_loss[i]) / d student[i]
+ *               = row_scale[i] T (q - sum_j p_j e_{ids[i][j]}).
+ * student [n][n_classes] of `dtype`, teacher_logits [n][k] fp32, teacher_ids
+ * [n][k] int32, out_loss [n] fp32, out_grad (may be NULL) [n][n_classes] of
+ * `dtype`, row_scale [n] fp32 (NULL: 1). An entry is kept when its id is in
+ * 0..n_classes-1 and its logit is not -inf; a row that keeps none has loss 0
+ * and gradient 0. An id given twice counts twice. A student logit of -inf has
+ * q = 0. 1 <= k <= 256, 1 <= n_classes <= 2^30, T > 0 and finite. */
+NERF_API nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n, int n_classes,
+                                       const float* teacher_logits, const int32_t* teacher_ids,
+                                       int k, float temperature, const float* row_scale,
+                                       float* out_loss, void* out_grad, void* stream);
+
+/* The KiloNeRF cell networks (nerf_params.cell_w) on rows sorted by cell:
+ * x, d [n_rows][3] fp32 (d normalised inside), offset [n_cells + 1] int32 as
+ * nerf_expert_sort writes it (rows offset[c] .. offset[c+1]-1 belong to cell c),
+ * cell_w [n_cells][3317]. out_raw [n_rows][4] = (r, g, b, sigma) before their
+ * activations; out_hidden (may be NULL) [n_rows][64]: the two hidden layers
+ * after ReLU, for the backward pass. Rows from offset[n_cells] on are left as
+ * they were. fp32 accuracy (tensor-core products split in three). n_rows <= 2^30. */
+NERF_API nerf_status nerf_cells_forward(const float* x, const float* d, int64_t n_rows,
+                                        const int32_t* offset, int n_cells, const float* cell_w,
+                                        float* out_raw, float* out_hidden, void* stream);
+
+/* Bytes of workspace that nerf_cells_backward needs for these sizes (host). */
+NERF_API nerf_status nerf_cells_backward_workspace(int64_t n_rows, int n_cells,
+                                                   int64_t* out_bytes);
+
+/* Weight gradient of nerf_cells_forward: x, d, offset, cell_w as in the forward
+ * pass, hidden [n_rows][64] as it wrote them (the hidden layers decide the ReLU
+ * masks, the derivative at 0 taken as 0), d_raw [n_rows][4]. grad_cell_w
+ * [n_cells][3317] is overwritten (0 for a cell without rows). Sums run in a
+ * fixed order: the result does not vary between runs. workspace as in
+ * nerf_expert_sort. */
+NERF_API nerf_status nerf_cells_backward(const float* x, const float* d, int64_t n_rows,
+                                         const int32_t* offset, int n_cells, const float* cell_w,
+                                         const float* hidden, const float* d_raw,
+                                         float* grad_cell_w, void* workspace,
+                                         int64_t workspace_bytes, void* stream);
+
 /* Real spherical harmonics of bands 0..3 (16 values, index l*l + l + m, no
  * Condon-Shortley phase) of the unit vectors d/|d|: the hash-grid MLP's view
  * encoding. The pages do not describe it; degree-4 real SH with the textbook

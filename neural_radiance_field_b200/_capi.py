@@ -23,6 +23,7 @@ NERF_MODEL_MLP, NERF_MODEL_KILONERF, NERF_MODEL_HASHGRID = 0, 1, 2
 NERF_SIGMA_RELU, NERF_SIGMA_SOFTPLUS = 0, 1
 NERF_FP32, NERF_BF16, NERF_TF32 = 0, 1, 2
 NERF_LAST_1E10, NERF_LAST_TO_FAR = 0, 1
+NERF_DTYPE_FP32, NERF_DTYPE_BF16, NERF_DTYPE_FP16 = 0, 1, 2
 TIMED_KINDS = ("network", "composite", "resample", "dir_bias", "march_mask", "march_compact",
                "router", "march_composite")           # NERF_TIMED_* order
 
@@ -86,6 +87,16 @@ SIGNATURES = {
     "nerf_test_route_cells": (_I, [_P, _I64, _P, _P, _P, _P, _P]),
     "nerf_test_hash_encode": (_I, [_P, _I64, _P, _P, _P, _P]),
     "nerf_hash_encode_backward": (_I, [_P, _I64, _P, _P, _I, _P]),
+    "nerf_expert_sort_workspace": (_I, [_I64, _I, _I, ctypes.POINTER(_I64)]),
+    "nerf_expert_sort": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P, _I64, _P]),
+    "nerf_expert_dispatch": (_I, [_P, _I, _I64, _I, _P, _I, _P, _P, _P]),
+    "nerf_expert_dispatch_backward": (_I, [_P, _P, _I, _I64, _I, _P, _I, _P, _P, _P, _P]),
+    "nerf_expert_combine": (_I, [_P, _I, _I64, _I, _P, _I, _P, _P, _P]),
+    "nerf_expert_combine_backward": (_I, [_P, _P, _I, _I64, _I, _P, _I, _P, _P, _P, _P]),
+    "nerf_distill_topk": (_I, [_P, _I, _I64, _I, _P, _P, _I, _F, _P, _P, _P, _P]),
+    "nerf_cells_forward": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _P]),
+    "nerf_cells_backward_workspace": (_I, [_I64, _I, ctypes.POINTER(_I64)]),
+    "nerf_cells_backward": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _P, _P, _I64, _P]),
     "nerf_test_sh": (_I, [_P, _I64, _P, _P]),
     "nerf_test_bounded_wait": (_I, [ctypes.c_uint32, _P, _P, _P]),
     "nerf_march_compact_noalloc": (_I, [_P, _P, _I64, _F, _F, _I, _P, _P, _P, _P]),

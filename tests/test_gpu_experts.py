@@ -1,0 +1,613 @@
+"""The expert operators on the GPU against the fp64 oracle, within bounds derived
+from the operations that each value goes through (u = 2^-24, the fp32 half step):
+every bound below is a worst case, element by element."""
+import numpy as np
+import pytest
+
+from nerf_inputs import kilonerf_weights
+from oracle import experts as E
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = ["fp32", "bf16", "fp16"]
+HALF_STEP = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+TINY = {"fp32": 2.0 ** -149, "bf16": 2.0 ** -133, "fp16": 2.0 ** -25}     # half a subnormal step at most
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    from neural_radiance_field_b200 import build
+    build.build()
+    return torch
+
+
+def _t(torch, dtype):
+    return {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _cuda(torch, a, dtype=None):
+    t = torch.from_numpy(np.array(a, order="C"))
+    return t.cuda() if dtype is None else t.cuda().to(dtype)
+
+
+def _near(got, ref, bound, name):
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{name}: {bad.sum()} of {bad.size}, worst {np.nanmax(np.abs(got - ref)):.3e}, " \
+                          f"at {np.argwhere(bad)[0]}: got {got[bad][0]!r}, want {ref[bad][0]!r}, bound {np.broadcast_to(bound, got.shape)[bad][0]:.3e}"
+
+
+def _ids(rng, n, k, e, drop=0.15):
+    """Distinct experts per point where there are enough, skewed; dropped pairs; some points all dropped."""
+    ids = (e * rng.random((n, 1)) ** 2 + np.arange(k) * max(1, e // k)).astype(np.int64) % e
+    ids[rng.random((n, k)) < drop] = -1
+    ids[rng.random(n) < drop] = -1
+    return ids.astype(np.int32)
+
+
+def _sorted(torch, ids, e, order=True):
+    import neural_radiance_field_b200 as nb
+    n, k = ids.shape
+    i32 = torch.int32
+    off = torch.full((e + 1,), -7, device="cuda", dtype=i32)
+    out = torch.full((n * k,), -7, device="cuda", dtype=i32) if order else None
+    pos = torch.full((n, k), -7, device="cuda", dtype=i32)
+    work = torch.empty(nb.nerf_expert_sort_workspace(n, k, e), device="cuda", dtype=torch.uint8)
+    nb.nerf_expert_sort(ids, e, off, out, pos, work)
+    return off, out, pos
+
+
+# ------------------------------------------------------------------ sort
+
+@pytest.mark.parametrize("n,k,e", [(1, 1, 1), (1, 8, 4096), (5, 3, 2), (31, 1, 7), (257, 2, 64), (1000, 8, 100),
+                                   (4096, 2, 4096), (4099, 5, 1000), (20011, 8, 4096), (9973, 64, 33), (300001, 2, 3)])
+@pytest.mark.parametrize("kind", ["mixed", "one expert", "all dropped"])
+def test_sort(torch, n, k, e, kind):
+    rng = np.random.default_rng([n, k, e])
+    if kind == "mixed":
+        ids = _ids(rng, n, k, e)
+        ids[rng.random((n, k)) < 0.01] = e            # past the last expert: dropped too
+        ids[rng.random((n, k)) < 0.01] = -(1 << 31)
+    else:
+        ids = np.full((n, k), e - 1 if kind == "one expert" else -1, np.int32)
+    off, order, pos = _sorted(torch, _cuda(torch, ids), e)
+    r_off, r_order, r_pos = E.sort(ids, e)
+    m = r_order.size
+    assert np.array_equal(off.cpu().numpy(), r_off)
+    assert np.array_equal(pos.cpu().numpy(), r_pos)
+    assert np.array_equal(order.cpu().numpy()[:m], r_order)
+    assert (order.cpu().numpy()[m:] == -7).all()        # behind the last kept pair: as it was
+    off2, _, pos2 = _sorted(torch, _cuda(torch, ids), e, order=False)
+    assert torch.equal(off, off2) and torch.equal(pos, pos2)
+
+
+def test_sort_agrees_with_the_cell_router(torch):
+    """One cell per point: the same counts and cells as nerf_test_route_cells."""
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng(0)
+    x = _cuda(torch, rng.uniform(-1.5, 1.4999, size=(5000, 3)).astype(np.float32))
+    i32 = torch.int32
+    cell = torch.empty(5000, device="cuda", dtype=i32)
+    cnt, off = torch.empty(4096, device="cuda", dtype=i32), torch.empty(4097, device="cuda", dtype=i32)
+    order = torch.empty(5000, device="cuda", dtype=i32)
+    nb.nerf_test_route_cells(x, cell, cnt, off, order)
+    mine, my_order, _ = _sorted(torch, cell[:, None].contiguous(), 4096)
+    assert torch.equal(mine, off)
+    assert torch.equal(cell[my_order.long()], cell[order.long()])
+
+
+# ------------------------------------------------------------------ rows
+
+def _rows_case(torch, rng, n, k, e, width, dtype, weighted, shift=0):
+    """Inputs on the device and, as read back from it, in fp64; `shift` elements off the 16-byte boundary."""
+    ids = _ids(rng, n, k, e)
+    pos = E.sort(ids, e)[2]
+    t = _t(torch, dtype)
+
+    def make(m):
+        flat = torch.empty(m * width + shift, device="cuda", dtype=t)
+        flat.copy_(_cuda(torch, rng.normal(size=m * width + shift)))
+        return flat[shift:].view(m, width)
+
+    w = rng.normal(size=(n, k)).astype(np.float32) if weighted else None
+    if weighted:
+        w[pos < 0] = np.nan                            # what lies in a dropped place is not looked at
+    return pos, _cuda(torch, pos.astype(np.int32)), w, None if w is None else _cuda(torch, w), make
+
+
+ROWS = [(1, 1, 1, 1), (1, 8, 4096, 4), (3, 2, 5, 3), (193, 2, 64, 63), (300, 8, 4096, 4), (257, 3, 17, 27), (64, 4, 8, 256),
+        (50, 2, 8, 1024), (100, 9, 16, 32), (33, 64, 100, 6), (20, 2, 4, 1023), (7, 12, 20, 2050), (40, 1, 3, 90)]
+
+
+@pytest.mark.parametrize("n,k,e,width", ROWS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("weighted,shift", [(True, 0), (False, 0), (True, 1), (True, 2)])
+def test_rows(torch, n, k, e, width, dtype, weighted, shift):
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng([n, k, e, width, TYPES.index(dtype), weighted, shift])
+    pos, pos_t, w, w_t, make = _rows_case(torch, rng, n, k, e, width, dtype, weighted, shift)
+    hs, tiny = HALF_STEP[dtype], TINY[dtype]
+    aw = np.where(pos >= 0, np.abs(w.astype(np.float64)) if weighted else 1.0, 0.0)
+    x, rows, old = make(n), make(n * k), make(n * k)
+    # dispatch: one product, rounded once to fp32 and once to the type; untouched rows keep their bits
+    got = old.clone() if shift == 0 else old
+    before = _np(got)
+    nb.nerf_expert_dispatch(x, pos_t, got, w_t)
+    ref = E.dispatch(_np(x), pos, w, before)
+    exact = np.ones(n * k, bool)
+    exact[pos[pos >= 0]] = not weighted
+    assert np.array_equal(_np(got)[exact], ref[exact])
+    _near(_np(got), ref, (U + hs + U * hs) * np.abs(ref) + tiny, "rows")
+    # combine: k fused steps in fp32 (each within u of the running sum), one rounding
+    out = make(n)
+    nb.nerf_expert_combine(rows, pos_t, out, w_t)
+    ref = E.combine(_np(rows), pos, w)
+    mag = (aw[..., None] * np.abs(E.taken(_np(rows), pos))).sum(1)
+    _near(_np(out), ref, hs * np.abs(ref) + (1 + hs) * 1.01 * k * U * mag + tiny, "out")
+    assert (_np(out)[(pos < 0).all(1)] == 0).all()
+    # their gradients; a dot product of `width` terms in any order: width * u of the sum of magnitudes
+    d_x, dw = make(n), torch.full((n, k), 7.0, device="cuda")
+    nb.nerf_expert_dispatch_backward(rows, x, pos_t, d_x, w_t, dw)
+    assert torch.equal(d_x, out)                       # the same sum as combine, whether or not d_weights is asked for
+    r_dw = E.dots(_np(rows), _np(x), pos)
+    b_dw = 1.01 * (width + 1) * U * (np.abs(E.taken(_np(rows), pos)) * np.abs(_np(x))[:, None]).sum(2) + TINY["fp32"]
+    _near(_np(dw), r_dw, b_dw, "d_weights")
+    assert (_np(dw)[pos < 0] == 0).all()
+    d_rows, dw2 = old.clone(), torch.full((n, k), 7.0, device="cuda")
+    d_rows.copy_(_cuda(torch, before))
+    if shift:
+        d_rows = make(n * k)
+        d_rows.copy_(_cuda(torch, before))
+    nb.nerf_expert_combine_backward(x, rows, pos_t, d_rows, w_t, dw2)
+    assert torch.equal(d_rows, got)                    # the same products as dispatch
+    _near(_np(dw2), r_dw, b_dw, "d_weights of combine")
+    # either output alone is the same
+    only = torch.full((n, k), 7.0, device="cuda")
+    nb.nerf_expert_dispatch_backward(rows, x, pos_t, None, w_t, only)
+    assert torch.equal(only, dw)
+    nb.nerf_expert_combine_backward(x, rows, pos_t, None, w_t, only)
+    assert torch.equal(only, dw2)
+    d_x2 = make(n)
+    nb.nerf_expert_dispatch_backward(rows, None, pos_t, d_x2, w_t, None)
+    assert torch.equal(d_x2, d_x)
+
+
+def test_rows_nonfinite(torch):
+    """An infinity or NaN in a kept row reaches its own point only; in rows that nothing names it reaches none."""
+    import neural_radiance_field_b200 as nb
+    pos = torch.tensor([[0, 1], [2, -1], [-1, -1]], device="cuda", dtype=torch.int32)
+    for width in (4, 5, 64):
+        for dtype in TYPES:
+            rows = torch.ones(6, width, device="cuda", dtype=_t(torch, dtype))
+            rows[3:] = float("nan")
+            rows[1, 2] = float("inf")
+            out = torch.empty(3, width, device="cuda", dtype=rows.dtype)
+            nb.nerf_expert_combine(rows, pos, out, torch.full((3, 2), 2.0, device="cuda"))
+            ref = torch.full((3, width), 2.0, device="cuda")
+            ref[0] = 4.0
+            ref[0, 2] = float("inf")
+            ref[2] = 0.0
+            assert torch.equal(out.float(), ref)
+
+
+def test_rows_positions_out_of_range_are_dropped(torch):
+    import neural_radiance_field_b200 as nb
+    pos = torch.tensor([[0, 4], [1 << 30, -(1 << 31)]], device="cuda", dtype=torch.int32)   # n * k = 4 rows
+    rows = torch.zeros(4, 8, device="cuda")
+    nb.nerf_expert_dispatch(torch.ones(2, 8, device="cuda"), pos, rows)
+    assert rows[0].eq(1).all() and rows[1:].eq(0).all()
+    out = torch.empty(2, 8, device="cuda")
+    nb.nerf_expert_combine(torch.full((4, 8), 3.0, device="cuda"), pos, out)
+    assert out[0].eq(3).all() and out[1].eq(0).all()
+
+
+# ------------------------------------------------------------------ distillation
+
+def _distill_bounds(s, teacher, ids, T, scale, loss, grad, k):
+    """Worst-case error of (loss, grad in fp32). z = s / T by the rounded 1/T: 2u |z|. The exponent's
+    argument z - m: 2u(|z| + |m|) + u|z - m| <= 6uA, A = max |z|; exp within 2 steps (4u). A sum of the
+    classes in at most classes / 32 + 16 steps. log within 2 steps of its value."""
+    z = s / T
+    n, e = s.shape
+    fin = np.where(np.isfinite(z), np.abs(z), 0.0)
+    A = fin.max(1)
+    d_exp = U * (6 * A + 4)
+    d_sum = d_exp + U * (e / 32 + 16)
+    lz = np.log(e) + 2 * A
+    d_logq = U * (4 * A + 2 * A) + d_sum + 4 * U * lz + 3 * U * (2 * A + lz)
+    kept = (ids >= 0) & (ids < e) & (teacher != -np.inf)
+    tz = np.where(kept, teacher / T, 0.0)
+    At = np.abs(tz).max(1)
+    d_p = U * (2 * (6 * At + 4) + k + 4)
+    d_logp = U * (4 * At + 2 * At) + U * (6 * At + 4 + k) + 8 * U * np.log(k + 1) + 3 * U * (2 * At + np.log(k + 1))
+    big = 2 * At + 2 * A + np.log(k + 1) + lz                      # |log p - log q| of a kept class
+    b_loss = 1.01 * T * T * (d_logq + d_logp + (d_p + U * (k + 4)) * big)
+    q = np.where(np.isfinite(z), np.exp(z - z.max(1, keepdims=True)), 0.0)
+    q /= q.sum(1, keepdims=True)
+    p = np.zeros((n, e))
+    for i in range(n):
+        if kept[i].any():
+            y = np.exp(tz[i][kept[i]] - tz[i][kept[i]].max())
+            np.add.at(p[i], ids[i][kept[i]], y / y.sum())
+    b_grad = 1.01 * np.abs(scale * T)[:, None] * (q * (d_exp + d_sum + 4 * U)[:, None] + p * (d_p + U * (k + 2))[:, None]
+                                                 + U * (q + p)) + 3 * U * np.abs(grad)
+    return b_loss, b_grad
+
+
+DISTILL = [(1, 1, 1), (1, 8, 4096), (5, 3, 2), (33, 8, 31), (64, 16, 100), (17, 5, 333), (9, 32, 1024), (20, 16, 4096),
+           (7, 256, 5000), (6, 9, 8191), (4, 32, 20001), (3, 40, 100003), (2, 7, 262144), (300, 2, 64)]
+
+
+@pytest.mark.parametrize("n,k,e", DISTILL)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_distill(torch, n, k, e, dtype, shift):
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng([n, k, e, TYPES.index(dtype)])
+    T = 1.5
+    t = _t(torch, dtype)
+    base = torch.empty(n * e + shift, device="cuda", dtype=t)
+    base.copy_(_cuda(torch, 2.5 * rng.normal(size=n * e + shift)))
+    student = base[shift:].view(n, e)
+    ids = np.stack([rng.choice(e, size=k, replace=e < k) for _ in range(n)]).astype(np.int32)
+    teacher = (3 * rng.normal(size=(n, k))).astype(np.float32)
+    if n > 1:
+        ids[rng.random((n, k)) < 0.2] = -1
+        ids[n // 2] = -1                               # a row that keeps nothing
+    if n > 2:
+        teacher[1, 0] = -np.inf                        # a kept place whose logit is masked
+        teacher[2] = -np.inf                           # a row whose logits all are
+        ids[0, 0] = ids[0, -1] = e - 1                 # an id twice (k = 1: once)
+        ids[3 % n, k // 2] = e                         # past the last class
+        masked = np.setdiff1d(rng.choice(e, size=e // 3, replace=False), ids[0])
+        student[0, _cuda(torch, masked)] = float("-inf")
+    scale = rng.random(n).astype(np.float32) + 0.5
+    args = (_cuda(torch, teacher), _cuda(torch, ids), T)
+    loss = torch.full((n,), 7.0, device="cuda")
+    gbase = torch.full((n * e + shift,), 7.0, device="cuda", dtype=t)
+    grad = gbase[shift:].view(n, e)
+    nb.nerf_distill_topk(student, *args, loss, grad, _cuda(torch, scale))
+    r_loss, r_grad = E.distill(_np(student), teacher.astype(np.float64), ids, T, scale)
+    b_loss, b_grad = _distill_bounds(_np(student), teacher.astype(np.float64), ids, T, scale.astype(np.float64), r_loss, r_grad, k)
+    _near(_np(loss), r_loss, b_loss, "loss")
+    hs = HALF_STEP[dtype]
+    _near(_np(grad), r_grad, (1 + hs) * b_grad + hs * np.abs(r_grad) + TINY[dtype], "grad")
+    if n > 2:
+        assert loss[2] == 0 and grad[2].eq(0).all()
+    if n > 1:
+        assert loss[n // 2] == 0 and grad[n // 2].eq(0).all()
+    if shift:
+        assert gbase[0] == 7.0
+    alone = torch.full((n,), 7.0, device="cuda")
+    nb.nerf_distill_topk(student, *args, alone)
+    assert torch.equal(alone, loss)
+    ones = torch.empty_like(grad)
+    nb.nerf_distill_topk(student, *args, alone, ones)
+    nb.nerf_distill_topk(student, *args, alone, grad, torch.ones(n, device="cuda"))
+    assert torch.equal(ones, grad)
+
+
+@pytest.mark.parametrize("e", [40, 4096, 20001])
+def test_distill_masks_and_extremes(torch, e):
+    """Masks of the lowest value and of -inf, a kept class that the student rules out, NaN in rows that
+    keep nothing, and rows beside each other that must not mix."""
+    import neural_radiance_field_b200 as nb
+    low = torch.finfo(torch.float32).min
+    s = torch.zeros(5, e, device="cuda")
+    s[0, 1:] = low                                      # all mass on class 0
+    s[1, 1:] = float("-inf")
+    s[2] = float("nan")
+    s[3, 0] = float("-inf")                            # the teacher's only class is ruled out
+    ids = torch.tensor([[0, -1], [0, -1], [-1, -1], [0, -1], [1, 2]], device="cuda", dtype=torch.int32)
+    tl = torch.zeros(5, 2, device="cuda")
+    loss, grad = torch.empty(5, device="cuda"), torch.empty(5, e, device="cuda")
+    nb.nerf_distill_topk(s, tl, ids, 1.0, loss, grad)
+    assert loss[:3].eq(0).all() and grad[:3].eq(0).all()
+    assert loss[3] == float("inf") and torch.isfinite(grad[3]).all() and grad[3, 0] == -1
+    want = np.log(e) - np.log(2)
+    assert abs(loss[4].item() - want) <= 20 * U * (np.log(e) + 2) + (e / 32 + 16) * U
+
+
+# ------------------------------------------------------------------ per-cell networks
+
+C3 = 1.25 * 2.0 ** -20      # a product of two operands split in three: lo parts read at 2^-10, lo * lo dropped
+
+
+def _encoding_errors(x, d):
+    """Bound on the encodings' errors: sin and cos of the exact angle within 2 steps (2^-23); the unit
+    direction's coordinates within 3.5u of their value, times the angle's slope."""
+    ex = np.concatenate([np.zeros((len(x), 3)), np.full((len(x), 60), 2.0 ** -23)], axis=1)
+    u = np.abs(d / np.linalg.norm(d, axis=1, keepdims=True))
+    slope = np.pi * 2.0 ** np.arange(4)
+    ang = (u[:, :, None] * slope).reshape(len(d), 12) * 3.5 * U
+    return ex, np.concatenate([u * 3.5 * U, ang + 2.0 ** -23, ang + 2.0 ** -23], axis=1)
+
+
+def _cells_case(torch, seed, counts, extra=0):
+    rng = np.random.default_rng(seed)
+    offset = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    n = int(offset[-1]) + extra
+    x = rng.uniform(-1.5, 1.5, size=(max(n, 1), 3)).astype(np.float32)
+    d = (rng.normal(size=(max(n, 1), 3)) * 3).astype(np.float32)
+    return rng, offset, x, d, kilonerf_weights(seed, n_cells=len(counts))
+
+
+COUNTS = {"one row": [1], "a tile less one": [0, 127], "a tile": [128, 0, 0], "a tile and one": [129, 3],
+          "ragged": [0, 1, 7, 64, 130, 0, 300, 31, 128, 257, 0], "no rows": [0, 0], "many small": [3] * 700,
+          "a hot cell": [5, 4000, 0, 2] + [1] * 30}
+
+
+@pytest.mark.parametrize("name", list(COUNTS))
+def test_cells(torch, name):
+    import neural_radiance_field_b200 as nb
+    counts = COUNTS[name]
+    rng, offset, x, d, w = _cells_case(torch, len(counts), counts, extra=5)
+    n, m = len(x), int(offset[-1])
+    xt, dt, ot, wt = (_cuda(torch, a) for a in (x, d, offset, w))
+    raw, hid = torch.full((n, 4), 7.0, device="cuda"), torch.full((n, 64), 7.0, device="cuda")
+    nb.nerf_cells_forward(xt, dt, ot, wt, raw, hid)
+    r_raw, r_hid = E.cells_forward(x, d, offset, w)
+    px, pd = E.encodings(x, d)
+    ex, ed = _encoding_errors(x, d.astype(np.float64))
+    b_raw, b_hid = np.zeros((n, 4)), np.zeros((n, 64))
+    for c in range(len(counts)):
+        r = slice(offset[c], offset[c + 1])
+        w1, b1, w2, b2, ws, bs, wc, bc = (np.abs(v) for v in E.cell_parts(w[c]))
+        h1, h2 = r_hid[r, :32], r_hid[r, 32:]
+        e1 = ex[r] @ w1.T + (C3 + 66 * U) * (np.abs(px[r]) @ w1.T + b1)
+        e2 = e1 @ w2.T + (C3 + 35 * U) * ((h1 + e1) @ w2.T + b2)
+        b_hid[r] = np.concatenate([e1, e2], axis=1)
+        both, eb = np.concatenate([h2, np.abs(pd[r])], axis=1), np.concatenate([e2, ed[r]], axis=1)
+        b_raw[r, :3] = eb @ wc.T + (C3 + 62 * U) * ((both + eb) @ wc.T + bc)
+        b_raw[r, 3] = e2 @ ws + (C3 + 35 * U) * ((h2 + e2) @ ws + bs)
+    _near(_np(hid)[:m], r_hid[:m], 1.01 * b_hid[:m] + 1e-30, "hidden")
+    _near(_np(raw)[:m], r_raw[:m], 1.01 * b_raw[:m] + 1e-30, "raw")
+    assert raw[m:].eq(7.0).all() and hid[m:].eq(7.0).all()       # rows behind the last: as they were
+    raw2 = torch.full((n, 4), 7.0, device="cuda")
+    nb.nerf_cells_forward(xt, dt, ot, wt, raw2)
+    assert torch.equal(raw, raw2)
+    # the weight gradient, from hidden layers as the forward wrote them
+    g = rng.normal(size=(n, 4)).astype(np.float32)
+    h = _np(hid)
+    h[m:] = 0
+    grad = torch.full((len(counts), E.N_CELL), 7.0, device="cuda")
+    work = torch.empty(nb.nerf_cells_backward_workspace(n, len(counts)), device="cuda", dtype=torch.uint8)
+    hid[m:] = float("nan")                               # not looked at
+    gt = _cuda(torch, g)
+    gt[m:] = float("nan")
+    nb.nerf_cells_backward(xt, dt, ot, wt, hid, gt, grad, work)
+    ref = E.cells_backward(x, d, offset, w, h, g)
+    bound = np.zeros_like(ref)
+    for c in range(len(counts)):
+        r = slice(offset[c], offset[c + 1])
+        _, _, w2, _, ws, _, wc, _ = E.cell_parts(w[c])
+        gc, gs = np.abs(g[r, :3].astype(np.float64)), np.abs(g[r, 3].astype(np.float64))
+        on1, on2 = h[r, :32] > 0, h[r, 32:] > 0
+        m2 = (gc @ np.abs(wc[:, :32]) + gs[:, None] * np.abs(ws)) * on2
+        e2 = (C3 + 5 * U) * m2
+        m1 = ((m2 + e2) @ np.abs(w2)) * on1
+        e1 = (e2 @ np.abs(w2)) * on1 + (C3 + 34 * U) * m1
+        acc = C3 + (counts[c] + 8) * U                   # a sum over the cell's rows, in any order
+        apx, both = np.abs(px[r]), np.concatenate([h[r, 32:], np.abs(pd[r])], axis=1)
+        eb = np.concatenate([np.zeros((counts[c], 32)), ed[r]], axis=1)
+        M1, M2 = m1 + e1, m2 + e2
+        one = np.ones((counts[c], 1))
+
+        def outer(a, ea, b, eb_):
+            return a.T @ eb_ + ea.T @ (b + eb_) + acc * (a.T @ (b + eb_))
+
+        z32, z1, z4 = np.zeros((counts[c], 32)), np.zeros((counts[c], 1)), np.zeros((counts[c], 3))
+        bound[c] = np.concatenate([
+            outer(M1, e1, apx, ex[r]).ravel(), outer(M1, e1, one, z1).ravel(), outer(M2, e2, h[r, :32], z32).ravel(),
+            outer(M2, e2, one, z1).ravel(), outer(gs[:, None], z1, h[r, 32:], z32).ravel(), outer(gs[:, None], z1, one, z1).ravel(),
+            outer(gc, z4, both, eb).ravel(), outer(gc, z4, one, z1).ravel()])
+    _near(_np(grad), ref, 1.01 * bound + 1e-30, "grad")
+    again = torch.full_like(grad, -3.0)
+    nb.nerf_cells_backward(xt, dt, ot, wt, hid, gt, again, work)
+    assert torch.equal(grad, again)
+
+
+def test_cells_agree_with_the_renderers_network(torch):
+    """sigma and rgb of one KiloNeRF frame: each ray marched by hand through nerf_test_march's live samples,
+    nerf_expert_sort and nerf_cells_forward composites to nerf_render's colour."""
+    import dataclasses
+    import nerf_inputs as S
+    import neural_radiance_field_b200 as nb
+    from oracle import nerf as onerf
+    wl = dataclasses.replace(S.WORKLOADS["kilonerf"], H=6, W=8, focal=10.0, ert_T=0.0)
+    packed, _ = S.occupancy_grid(7)
+    w = kilonerf_weights(8)
+    o, d = onerf.raygen(wl.H, wl.W, wl.focal, wl.c2w())
+    o, d = _cuda(torch, o), _cuda(torch, d)
+    occ, wt, R = _cuda(torch, packed.view(np.int32)).view(torch.uint32), _cuda(torch, w), wl.n_rays
+    with nb.Renderer(model=nb.NERF_MODEL_KILONERF, max_rays=R, max_samples=wl.n_coarse) as rnd:
+        p = rnd.params(occupancy=occ, cell_w=wt, march_step=wl.march_step, ert_T=0.0)
+        rgb, dep, acc = torch.empty(R, 3, device="cuda"), torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
+        rnd.render(o, d, wl.near, wl.far, wl.n_coarse, 0, p, rgb, dep, acc)
+        rnd.sync_status()
+    cnt, live = torch.empty(R, device="cuda", dtype=torch.int32), torch.empty(R, wl.n_coarse, device="cuda", dtype=torch.uint8)
+    nb.nerf_test_march(o, d, wl.near, wl.march_step, wl.n_coarse, occ, cnt, live)
+    ray, k = live.nonzero(as_tuple=True)
+    t = torch.tensor(wl.near, device="cuda") + k.float() * torch.tensor(wl.march_step, device="cuda")
+    x = o[ray] + t[:, None] * d[ray]
+    n = x.shape[0]
+    assert n > 300
+    cell = torch.empty(n, device="cuda", dtype=torch.int32)
+    i32 = torch.int32
+    nb.nerf_test_route_cells(x.contiguous(), cell, torch.empty(4096, device="cuda", dtype=i32), torch.empty(4097, device="cuda", dtype=i32))
+    off, _, pos = _sorted(torch, cell[:, None].contiguous(), 4096)
+    xs, ds, raws, raw = (torch.empty(n, c, device="cuda") for c in (3, 3, 4, 4))
+    nb.nerf_expert_dispatch(x.contiguous(), pos, xs)
+    nb.nerf_expert_dispatch(d[ray].contiguous(), pos, ds)
+    nb.nerf_cells_forward(xs, ds, off, wt, raws)
+    nb.nerf_expert_combine(raws, pos, raw)
+    a = raw.double()
+    delta = wl.march_step * d.double().norm(dim=1)[ray]
+    tau = a[:, 3].clamp_min(0) * delta
+    total = torch.zeros(R, device="cuda", dtype=torch.float64)
+    want = torch.zeros(R, 3, device="cuda", dtype=torch.float64)
+    start = 0
+    for r, c in enumerate(cnt.tolist()):
+        s = slice(start, start + c)
+        T = torch.exp(-(tau[s].cumsum(0) - tau[s]))
+        want[r] = ((T * -torch.expm1(-tau[s]))[:, None] * torch.sigmoid(a[s, :3])).sum(0)
+        start += c
+    # the parity bar of the fp32 render; both sides are within it of the same field
+    assert (rgb.double() - want).abs().max() <= 1e-4
+
+
+# ------------------------------------------------------------------ together
+
+def _mixture(torch, seed, n=400, k=3, e=6):
+    """A mixture over e cell networks: gate logits -> top k -> sort -> networks -> weighted blend."""
+    rng = np.random.default_rng(seed)
+    logits = rng.normal(size=(n, e))
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :k].astype(np.int32)
+    ids[rng.random((n, k)) < 0.1] = -1
+    ids[5] = -1
+    w = rng.random((n, k)).astype(np.float32)
+    x, d = rng.uniform(-1.5, 1.5, size=(n, 3)).astype(np.float32), rng.normal(size=(n, 3)).astype(np.float32)
+    return rng, ids, w, x, d, kilonerf_weights(seed, n_cells=e)
+
+
+class _Step:
+    """One training step of the mixture with its buffers; run() only enqueues."""
+
+    def __init__(self, torch, ids, w, x, d, cells, G):
+        import neural_radiance_field_b200 as nb
+        n, k = ids.shape
+        e, m = len(cells), n * k
+        self.torch, self.nb, self.e = torch, nb, e
+        self.ids, self.w, self.x, self.d, self.cells, self.G = (_cuda(torch, a) for a in (ids, w, x, d, cells, G))
+        z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+        i32 = torch.int32
+        self.off, self.pos = z(e + 1).to(i32), z(n, k).to(i32)
+        self.xs, self.ds, self.raws, self.hid, self.out = z(m, 3), z(m, 3), z(m, 4), z(m, 64), z(n, 4)
+        self.d_raws, self.dw, self.grad = z(m, 4), z(n, k), z(e, E.N_CELL)
+        self.sw = torch.empty(nb.nerf_expert_sort_workspace(n, k, e), device="cuda", dtype=torch.uint8)
+        self.cw = torch.empty(nb.nerf_cells_backward_workspace(m, e), device="cuda", dtype=torch.uint8)
+
+    def run(self, stream=None):
+        nb, a = self.nb, dict(stream=stream)
+        nb.nerf_expert_sort(self.ids, self.e, self.off, None, self.pos, self.sw, **a)
+        nb.nerf_expert_dispatch(self.x, self.pos, self.xs, **a)
+        nb.nerf_expert_dispatch(self.d, self.pos, self.ds, **a)
+        nb.nerf_cells_forward(self.xs, self.ds, self.off, self.cells, self.raws, self.hid, **a)
+        nb.nerf_expert_combine(self.raws, self.pos, self.out, self.w, **a)
+        nb.nerf_expert_combine_backward(self.G, self.raws, self.pos, self.d_raws, self.w, self.dw, **a)
+        nb.nerf_cells_backward(self.xs, self.ds, self.off, self.cells, self.hid, self.d_raws, self.grad, self.cw, **a)
+
+    def results(self):
+        return [t.clone() for t in (self.out, self.dw, self.grad)]
+
+
+def test_a_training_step_of_a_mixture(torch):
+    """The whole chain against the oracle's chain and against differences of its loss."""
+    rng, ids, w, x, d, cells = _mixture(torch, 3)
+    n, k = ids.shape
+    G = rng.normal(size=(n, 4)).astype(np.float32)
+    step = _Step(torch, ids, w, x, d, cells, G)
+    step.run()
+    out, dw, grad = (_np(t) for t in step.results())
+    off, order, pos = E.sort(ids, len(cells))
+    zero = np.zeros((n * k, 3))
+
+    def chain(w, cells):
+        xs, ds = E.dispatch(x, pos, None, zero), E.dispatch(d, pos, None, np.ones((n * k, 3)))
+        raws, hid = E.cells_forward(xs, ds, off, cells)
+        return E.combine(raws, pos, w), raws, hid, xs, ds
+
+    r_out, raws, hid, xs, ds = chain(w.astype(np.float64), cells.astype(np.float64))
+    # measured values of O(1) through three fp32 layers: 1e-4 of the largest, the bar of the fp32 parity tests
+    assert np.abs(out - r_out).max() <= 1e-4 * np.abs(r_out).max() and (out[5] == 0).all()
+    r_dw = E.dots(raws, G, pos)
+    assert np.abs(dw - r_dw).max() <= 1e-4 * np.abs(r_dw).max()
+    d_raws = E.dispatch(G, pos, w, np.zeros((n * k, 4)))
+    r_grad = E.cells_backward(xs, ds, off, cells, hid, d_raws)
+    assert np.abs(grad - r_grad).max() <= 1e-4 * np.abs(r_grad).max()
+    for q in rng.integers(0, E.N_CELL, size=6).tolist() + [3314]:
+        hi, lo = cells.astype(np.float64), cells.astype(np.float64)
+        hi[1, q] += 1e-6
+        lo[1, q] -= 1e-6
+        num = ((chain(w, hi)[0] - chain(w, lo)[0]) * G).sum() / 2e-6
+        assert abs(num - grad[1, q]) <= 1e-4 * np.abs(r_grad).max() + 1e-5
+
+
+def test_two_steps_on_two_streams_and_a_captured_one(torch):
+    """Steps that overlap on two streams, and a step replayed from a CUDA graph on new inputs while another
+    runs, give what each gives alone."""
+    steps, want = [], []
+    for seed in (11, 12):
+        rng, ids, w, x, d, cells = _mixture(torch, seed, n=3000)
+        G = rng.normal(size=(3000, 4)).astype(np.float32)
+        steps.append(_Step(torch, ids, w, x, d, cells, G))
+        steps[-1].run()
+        want.append(steps[-1].results())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in steps:
+        s.out.zero_(), s.grad.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, st in zip(steps, streams):
+            s.run(stream=st)
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        assert all(torch.equal(a, b) for a, b in zip(s.results(), w))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        steps[0].run()
+    for t in ("ids", "w", "x", "d", "cells", "G"):       # the graph reads these buffers: the other step's inputs
+        getattr(steps[0], t).copy_(getattr(steps[1], t))
+    steps[0].out.zero_(), steps[0].grad.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    steps[1].run(stream=streams[1])
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(steps[0].results(), want[1]))
+    assert all(torch.equal(a, b) for a, b in zip(steps[1].results(), want[1]))
+
+
+def test_a_gate_learns_from_its_teachers_top_logits(torch):
+    """The gate's logits step along the distillation gradient; what the kernel returns is the gradient of the
+    summed loss along that direction, by differences of the oracle's loss."""
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng(21)
+    n, e, k = 200, 512, 8
+    s, teacher = rng.normal(size=(n, e)).astype(np.float32), (2 * rng.normal(size=(n, k))).astype(np.float32)
+    ids = np.stack([rng.permutation(e)[:k] for _ in range(n)]).astype(np.int32)
+    loss, grad = torch.empty(n, device="cuda"), torch.empty(n, e, device="cuda")
+    nb.nerf_distill_topk(_cuda(torch, s), _cuda(torch, teacher), _cuda(torch, ids), 2.0, loss, grad)
+    g = _np(grad)
+    f = lambda a: E.distill(s.astype(np.float64) + a * g, teacher.astype(np.float64), ids, 2.0)[0].sum()  # noqa: E731
+    # central difference of a smooth function: error h^2 |f'''| / 6 with h = 1e-3 and |f'''| <= 8 sum|g|^3 / T
+    num, dot = (f(1e-3) - f(-1e-3)) / 2e-3, (g * g).sum()
+    assert abs(num - dot) <= 1e-6 * 8 * (np.abs(g).sum(1) ** 3).sum() + 1e-5 * dot
+
+
+def test_offsets_past_32_bits(torch):
+    """Rows whose byte and element offsets pass 2^32."""
+    import neural_radiance_field_b200 as nb
+    n, width = 4200, 1 << 20
+    x = torch.zeros(n, width, device="cuda", dtype=torch.bfloat16)             # 4.4e9 elements, 8.8 GB
+    x[-1] = 3.0
+    x[0, -1] = 5.0
+    pos = torch.arange(n - 1, -1, -1, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    rows = torch.zeros_like(x)
+    nb.nerf_expert_dispatch(x, pos, rows)
+    assert rows[0].eq(3).all() and rows[-1, -1] == 5 and rows[-1, :-1].eq(0).all() and rows[n // 2].eq(0).all()
+    x.zero_()
+    nb.nerf_expert_combine(rows, pos, x)
+    assert x[-1].eq(3).all() and x[0, -1] == 5 and x[0, :-1].eq(0).all()
+    loss = torch.empty(n, device="cuda")
+    tl, ti = torch.zeros(n, 1, device="cuda"), torch.full((n, 1), width - 1, device="cuda", dtype=torch.int32)
+    nb.nerf_distill_topk(x, tl, ti, 1.0, loss, rows)
+    # row 0: q of the class is e^5 / (2^20 - 1 + e^5) = 1.4e-4, and -(1 - 1.4e-4) is nearest to -1 among bf16
+    # values (the next is -1 + 2^-8); the other classes have q = 1 / (2^20 - 1 + e^5), in row 0 and (3s alone) 2^-20
+    assert rows[-1, -1] == -1 and rows[0, -1] == -1 and torch.isfinite(loss).all()
+    assert abs(rows[0, 0].item() * (width - 1 + np.exp(5)) - 1) <= 2.0 ** -8 and rows[-1, :-1].eq(2.0 ** -20).all()
