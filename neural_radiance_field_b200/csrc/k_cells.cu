@@ -4,141 +4,721 @@
 // Backward, with g = d raw: g2 = (Wc_h^T g_rgb + ws g_sigma) (h2 > 0),
 // g1 = (W2^T g2) (h1 > 0), and each weight's gradient the sum over the cell's
 // rows of (its output's gradient) x (its input).
+//
+// The products run as mma.sync m16n8k8 in tf32, three per product of two fp32
+// operands (v = hi + lo, hi rounded to tf32: hi*hi + hi*lo + lo*hi), which keeps
+// fp32 accuracy. The layers are 32 wide, so what decides is where the
+// activations live between them: a warp's fragments stay in its registers from
+// the encoding to the heads, the output fragment of one layer being the operand
+// fragment of the next under a permutation of the weight columns, and nothing
+// of a row passes through shared memory or a barrier. Lane l of a warp is
+// (g = l / 4, t = l % 4): operand A (16 x 8) holds rows g, g + 8 and columns t,
+// t + 4; B (8 x 8) rows t, t + 4 and column g; C (16 x 8) rows g, g + 8 and
+// columns 2t, 2t + 1. An angle's sine and cosine are a pair of fragment columns,
+// and the columns are ordered so that a lane that has an even octave has the odd
+// one above it too: sin 2a = 2 sin a cos a and cos 2a = 1 - 2 sin^2 a, four
+// operations in place of a second sincospif (about 35). With base q = 0..14
+// (coordinate q / 5, octave 2 (q % 5)), base 15 stands for x, y, z and a constant.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
 namespace {
 
-constexpr int CT = 256;
 // parameter offsets inside a cell's blob
 constexpr int O_W1 = 0, O_B1 = 2016, O_W2 = 2048, O_B2 = 3072, O_WS = 3104, O_BS = 3136, O_WC = 3137,
               O_BC = 3314;
-constexpr int CF_ROWS = 8;      // rows of one CTA at a time
 
-// unit direction: one rounded division per coordinate by the rounded norm
-__device__ __forceinline__ void unit3(const float* d, float* u) {
-  const float len = sqrtf(fmaf(d[0], d[0], fmaf(d[1], d[1], d[2] * d[2])));
-  u[0] = d[0] / len;
-  u[1] = d[1] / len;
-  u[2] = d[2] / len;
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float pe_value(const float* v, int octaves, int j) {
-  if (j < 3) return v[j];
-  const int q = (j - 3) % (3 * octaves);
-  float s, c;
-  pe_sincos(v[q / octaves], q % octaves, &s, &c);
-  return j - 3 < 3 * octaves ? s : c;
+// v = hi + lo: hi the nearest tf32 (10 stored bits, ties away from zero), lo exact;
+// the tensor core reads lo at tf32 precision.
+__device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(__fsub_rn(v, __uint_as_float(hi)));
+}
+// 1 / |d| as the divisor's reciprocal is not taken: each coordinate needed is
+// divided once by the rounded norm.
+__device__ __forceinline__ float norm3(const float* d) {
+  return sqrtf(fmaf(d[0], d[0], fmaf(d[1], d[1], d[2] * d[2])));
+}
+// v = (sin, cos) of octave k of coordinate xc, then of octave k + 1
+__device__ __forceinline__ void two_octaves(float xc, int k, float* v) {
+  sincospif(xc * __int_as_float((127 + k) << 23), v, v + 1);
+  const float s2 = v[0] + v[0];
+  v[2] = s2 * v[1];
+  v[3] = fmaf(-s2, v[0], 1.0f);
+}
+// base q of the position encoding: (sin, cos) of two octaves, or x, y, z, one
+__device__ __forceinline__ void position_base(const float* x, int q, float one, float* v) {
+  const int c = (q >= 5) + (q >= 10), k = 2 * (q - 5 * c);
+  two_octaves(c == 0 ? x[0] : c == 1 ? x[1] : x[2], k & 15, v);
+  if (q == 15) {
+    v[0] = x[0];
+    v[1] = x[1];
+    v[2] = x[2];
+    v[3] = one;
+  }
+}
+// column of gamma(x) that entry i (sin, cos, sin, cos) of base q stands for; 63 the constant
+__device__ __forceinline__ int position_column(int q, int i) {
+  const int c = (q >= 5) + (q >= 10), k = 2 * (q - 5 * c) + (i >> 1);
+  return q < 15 ? 3 + 30 * (i & 1) + 10 * c + k : i < 3 ? i : 63;
 }
 
-// One CTA per cell, CF_ROWS rows at a time, thread = (row, output).
-__global__ void __launch_bounds__(CT)
+// first[c] = tiles of `rows` rows of the cells before c, first[n_cells] = all of
+// them: each warp scans a run of cells, 32 at a time. Offsets are taken into
+// 0..n and sums kept below 2^30, so no table makes a row index leave its buffer.
+constexpr int TILES_MOST = 1 << 30;
+template <int THREADS>
+__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ offset, int64_t n,
+                                            int n_cells, int rows, int* first) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int sums[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (n_cells + WARPS * 32 - 1) / (WARPS * 32) * 32, base = warp * per;
+  auto at = [&](int c) { return (int)min(max((int64_t)__ldg(offset + c), (int64_t)0), n); };
+  int carry = 0;
+  for (int i0 = 0; i0 < per && base + i0 < n_cells; i0 += 256) {
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = base + i0 + 32 * i + lane;
+      v[i] = 32 * i + i0 < per && c < n_cells ? (max(at(c + 1) - at(c), 0) + rows - 1) / rows : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int run = v[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run = min(run + u, TILES_MOST);
+      }
+      const int c = base + i0 + 32 * i + lane;
+      if (32 * i + i0 < per && c < n_cells) first[c] = min(carry + run - v[i], TILES_MOST);
+      carry = min(carry + __shfl_sync(0xffffffffu, run, 31), TILES_MOST);
+    }
+  }
+  if (lane == 0) sums[warp] = carry;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w == warp) before = all;
+    all = min(all + sums[w], TILES_MOST);
+  }
+  for (int c = base + lane; c < min(base + per, n_cells); c += 32) first[c] = min(first[c] + before, TILES_MOST);
+  if (threadIdx.x == 0) first[n_cells] = all;
+  __syncthreads();
+}
+// the cell of a tile: first[c] <= tile < first[c + 1]
+__device__ __forceinline__ int cell_of(const int* first, int n_cells, int tile) {
+  int lo = 0, hi = n_cells;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= tile) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ forward
+
+constexpr int CF_WARPS = 4, CF_THREADS = CF_WARPS * 32;
+constexpr int CF_ROWS = CF_WARPS * 32;       // rows of a tile, 32 per warp
+constexpr int CF_PER_SM = 4;
+struct CellsForwardShared {
+  float4 w1[8 * 4 * 32];      // B fragments of W1: [k step][n tile][lane] = (hi, hi, lo, lo)
+  float4 w2[4 * 4 * 32];
+  float4 wh[32], wd[27], bh;  // heads (r, g, b, sigma) on h2 and (r, g, b, 0) on gamma(d)
+  float b1[32], b2[32];
+  int first[EXPERT_MAX + 1];
+};
+
+__device__ __forceinline__ float4 b_fragment(float b0, float b1) {
+  uint32_t h0, l0, h1, l1;
+  split3(b0, h0, l0);
+  split3(b1, h1, l1);
+  return make_float4(__uint_as_float(h0), __uint_as_float(h1), __uint_as_float(l0), __uint_as_float(l1));
+}
+
+__global__ void __launch_bounds__(CF_THREADS, CF_PER_SM)
 cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, int64_t n,
-                     const int32_t* __restrict__ offset, const float* __restrict__ cell_w,
-                     float* __restrict__ raw, float* __restrict__ hidden) {
-  __shared__ float w[CELL_NP], px[CF_ROWS][63], pd[CF_ROWS][27], h1[CF_ROWS][32], h2[CF_ROWS][32];
-  const int cell = blockIdx.x, t = threadIdx.x;
-  const int64_t a = max(offset[cell], 0), b = min((int64_t)offset[cell + 1], n);
-  if (a >= b) return;
-  for (int q = t; q < CELL_NP; q += CT) w[q] = cell_w[(int64_t)cell * CELL_NP + q];
-  const int r = t / 32, o = t & 31;
-  for (int64_t i0 = a; i0 < b; i0 += CF_ROWS) {
-    __syncthreads();
-    const bool on = i0 + r < b;
-    if (on) {
-      const float* v = x + (i0 + r) * 3;
-      float u[3];
-      unit3(d + (i0 + r) * 3, u);
-      for (int j = o; j < 63; j += 32) px[r][j] = pe_value(v, 10, j);
-      if (o < 27) pd[r][o] = pe_value(u, 4, o);
+                     const int32_t* __restrict__ offset, int n_cells,
+                     const float* __restrict__ cell_w, float* __restrict__ raw,
+                     float* __restrict__ hidden) {
+  extern __shared__ __align__(16) uint8_t cells_sm[];
+  CellsForwardShared& S = *reinterpret_cast<CellsForwardShared*>(cells_sm);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  tile_prefix<CF_THREADS>(offset, n, n_cells, CF_ROWS, S.first);
+  const int tiles = S.first[n_cells], per = (tiles + gridDim.x - 1) / gridDim.x;
+  const int end = min(tiles, (int)(blockIdx.x + 1) * per);
+  int staged = -1;
+  for (int tile = blockIdx.x * per; tile < end; ++tile) {
+    const int cell = cell_of(S.first, n_cells, tile);
+    if (cell != staged) {
+      staged = cell;
+      __syncthreads();                       // the previous cell's weights are no longer read
+      const float* __restrict__ W = cell_w + (int64_t)cell * CELL_NP;
+#pragma unroll
+      for (int q = tid; q < 8 * 4 * 32; q += CF_THREADS) {
+        const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), s = q >> 7;
+        const int base = 4 * (s >> 1) + (l & 3), c1 = position_column(base, 2 * (s & 1) + 1);
+        S.w1[q] = b_fragment(__ldg(W + nn * 63 + position_column(base, 2 * (s & 1))),
+                             c1 < 63 ? __ldg(W + nn * 63 + c1) : 0.0f);
+      }
+#pragma unroll
+      for (int q = tid; q < 4 * 4 * 32; q += CF_THREADS) {
+        const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), f = 8 * (q >> 7) + 2 * (l & 3);
+        S.w2[q] = b_fragment(__ldg(W + O_W2 + nn * 32 + f), __ldg(W + O_W2 + nn * 32 + f + 1));
+      }
+      if (tid < 32) {
+        S.b1[tid] = __ldg(W + O_B1 + tid);
+        S.b2[tid] = __ldg(W + O_B2 + tid);
+      } else if (tid < 64) {
+        const int f = tid - 32;
+        S.wh[f] = make_float4(__ldg(W + O_WC + f), __ldg(W + O_WC + 59 + f), __ldg(W + O_WC + 118 + f),
+                              __ldg(W + O_WS + f));
+      } else if (tid < 91) {
+        const int f = tid - 64 + 32;
+        S.wd[tid - 64] = make_float4(__ldg(W + O_WC + f), __ldg(W + O_WC + 59 + f),
+                                     __ldg(W + O_WC + 118 + f), 0.0f);
+      } else if (tid == 91) {
+        S.bh = make_float4(__ldg(W + O_BC), __ldg(W + O_BC + 1), __ldg(W + O_BC + 2), __ldg(W + O_BS));
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (on) {
-      float s = w[O_B1 + o];
-      for (int k = 0; k < 63; ++k) s = fmaf(w[O_W1 + o * 63 + k], px[r][k], s);
-      h1[r][o] = fmaxf(s, 0.0f);
+    // this warp's 32 rows: lane (g, t) works on rows g + 8 r, r = 0..3
+    const int64_t cell_begin = min(max((int64_t)offset[cell], (int64_t)0), n);
+    const int64_t cell_end = min(max((int64_t)offset[cell + 1], (int64_t)0), n);
+    const int64_t row0 = cell_begin + (int64_t)max(tile - S.first[cell], 0) * CF_ROWS + warp * 32;
+    if (row0 >= cell_end) continue;
+    int64_t row[4];
+    float px[4][3];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      row[r] = min(row0 + g + 8 * r, cell_end - 1);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) px[r][c] = x[row[r] * 3 + c];
     }
-    __syncthreads();
-    if (on) {
-      float s = w[O_B2 + o];
-      for (int k = 0; k < 32; ++k) s = fmaf(w[O_W2 + o * 32 + k], h1[r][k], s);
-      h2[r][o] = fmaxf(s, 0.0f);
-      if (hidden) {
-        hidden[(i0 + r) * 64 + o] = h1[r][o];
-        hidden[(i0 + r) * 64 + 32 + o] = h2[r][o];
+    float h[2][4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 b = *reinterpret_cast<const float2*>(&S.b1[8 * j + 2 * t]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        h[m][j][0] = h[m][j][2] = b.x;
+        h[m][j][1] = h[m][j][3] = b.y;
       }
     }
-    __syncthreads();
-    if (on && o < 4) {
-      float s = o < 3 ? w[O_BC + o] : w[O_BS];
-      const float* wr = o < 3 ? w + O_WC + o * 59 : w + O_WS;
-      for (int k = 0; k < 32; ++k) s = fmaf(wr[k], h2[r][k], s);
-      if (o < 3)
-        for (int k = 0; k < 27; ++k) s = fmaf(wr[32 + k], pd[r][k], s);
-      raw[(i0 + r) * 4 + o] = s;
+    // two k steps at a time: a base octave and the one above it. Not unrolled: the
+    // code of a whole tile would overrun the instruction cache.
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      uint32_t ah[2][2][4], al[2][2][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v[4];
+        position_base(px[r], 4 * b + t, 0.0f, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          split3(v[i], ah[i >> 1][r >> 1][2 * (i & 1) + (r & 1)], al[i >> 1][r >> 1][2 * (i & 1) + (r & 1)]);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 w = S.w1[((2 * b + s) * 4 + j) * 32 + lane];
+          const uint32_t bh0 = __float_as_uint(w.x), bh1 = __float_as_uint(w.y),
+                         bl0 = __float_as_uint(w.z), bl1 = __float_as_uint(w.w);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma_tf32(h[m][j], al[s][m], bh0, bh1);
+            mma_tf32(h[m][j], ah[s][m], bl0, bl1);
+            mma_tf32(h[m][j], ah[s][m], bh0, bh1);
+          }
+        }
+    }
+    float h2[2][4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 b = *reinterpret_cast<const float2*>(&S.b2[8 * j + 2 * t]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        h2[m][j][0] = h2[m][j][2] = b.x;
+        h2[m][j][1] = h2[m][j][3] = b.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[m][j][i] = fmaxf(h[m][j][i], 0.0f);
+        if (hidden) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (row0 + g + 8 * (2 * m + i) < cell_end)
+              *reinterpret_cast<float2*>(hidden + row[2 * m + i] * 64 + 8 * j + 2 * t) =
+                  make_float2(h[m][j][2 * i], h[m][j][2 * i + 1]);
+        }
+      }
+    }
+    // h1's fragment (row, columns 8s + 2t, 8s + 2t + 1) is the operand of k step
+    // s with its columns t, t + 4 standing for those two features
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t ah[2][4], al[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(h[m][s][i], ah[m][(i & 1) * 2 + (i >> 1)], al[m][(i & 1) * 2 + (i >> 1)]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = S.w2[(s * 4 + j) * 32 + lane];
+        const uint32_t bh0 = __float_as_uint(w.x), bh1 = __float_as_uint(w.y),
+                       bl0 = __float_as_uint(w.z), bl1 = __float_as_uint(w.w);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma_tf32(h2[m][j], al[m], bh0, bh1);
+          mma_tf32(h2[m][j], ah[m], bl0, bl1);
+          mma_tf32(h2[m][j], ah[m], bh0, bh1);
+        }
+      }
+    }
+    // the heads on the FMA pipe, which the tensor products leave idle: each lane
+    // its eight features of h2 and its share of gamma(d), for four rows
+    float o[4][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 w0 = S.wh[8 * j + 2 * t], w1 = S.wh[8 * j + 2 * t + 1];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float a = fmaxf(h2[r >> 1][j][2 * (r & 1)], 0.0f), b = fmaxf(h2[r >> 1][j][2 * (r & 1) + 1], 0.0f);
+        if (hidden && row0 + g + 8 * r < cell_end)
+          *reinterpret_cast<float2*>(hidden + row[r] * 64 + 32 + 8 * j + 2 * t) = make_float2(a, b);
+        o[r][0] = fmaf(w0.x, a, fmaf(w1.x, b, o[r][0]));
+        o[r][1] = fmaf(w0.y, a, fmaf(w1.y, b, o[r][1]));
+        o[r][2] = fmaf(w0.z, a, fmaf(w1.z, b, o[r][2]));
+        o[r][3] = fmaf(w0.w, a, fmaf(w1.w, b, o[r][3]));
+      }
+    }
+    // lane t < 3 has coordinate t of the direction and its four octaves
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float dd[3] = {d[row[r] * 3], d[row[r] * 3 + 1], d[row[r] * 3 + 2]};
+      const float ut = (t == 0 ? dd[0] : t == 1 ? dd[1] : dd[2]) / norm3(dd);
+      float v[8];
+      two_octaves(ut, 0, v);
+      two_octaves(ut, 2, v + 4);
+      if (t < 3) {
+        const float4 wu = S.wd[t];
+        o[r][0] = fmaf(wu.x, ut, o[r][0]);
+        o[r][1] = fmaf(wu.y, ut, o[r][1]);
+        o[r][2] = fmaf(wu.z, ut, o[r][2]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 a = S.wd[3 + 12 * (i & 1) + 4 * t + (i >> 1)];
+          o[r][0] = fmaf(a.x, v[i], o[r][0]);
+          o[r][1] = fmaf(a.y, v[i], o[r][1]);
+          o[r][2] = fmaf(a.z, v[i], o[r][2]);
+        }
+      }
+    }
+    // sum over the four lanes of a row; lane t keeps row g + 8 t
+    float4 v;
+    float* vp = &v.x;
+    const bool up = t & 2, odd = t & 1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float k0 = up ? o[2][c] : o[0][c], k1 = up ? o[3][c] : o[1][c];
+      const float s0 = up ? o[0][c] : o[2][c], s1 = up ? o[1][c] : o[3][c];
+      const float p0 = k0 + __shfl_xor_sync(0xffffffffu, s0, 2);
+      const float p1 = k1 + __shfl_xor_sync(0xffffffffu, s1, 2);
+      vp[c] = (odd ? p1 : p0) + __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+    }
+    const float4 bh = S.bh;
+    if (row0 + g + 8 * t < cell_end)
+      reinterpret_cast<float4*>(raw)[row0 + g + 8 * t] =
+          make_float4(v.x + bh.x, v.y + bh.y, v.z + bh.z, v.w + bh.w);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+
+// Two roles share the rows: a warp of the first computes g1 and the gradient of
+// W1 and b1 (64 accumulators a lane), one of the second the gradients of W2, b2
+// and the heads (48). Together they would take 252 registers and leave eight
+// warps to an SM; apart, twelve fit. Each role cuts all tiles of 16 rows into
+// one contiguous range per warp.
+// The tensor core truncates when it adds to an accumulator, an error that grows
+// with the number of additions and all in one direction (2e-6 of the gradient
+// at 370 rows a cell); so a tile's products go to a fresh accumulator, which is
+// added to the cell's by a rounded addition.
+constexpr int CB_A = 8, CB_B = 4;             // warps of each role in a CTA
+constexpr int CB_THREADS = (CB_A + CB_B) * 32;
+constexpr int CB_ROWS = 16;
+constexpr int CB_SMS = 148;
+constexpr int CB_NA = O_W2, CB_NB = CELL_NP - O_W2;   // parameters of each role
+struct CellsBackwardShared {
+  // A fragments of W2^T, [m tile][k step][lane], hi and lo; heads (r, g, b, sigma) on h2
+  uint4 hi[CB_A][2 * 4 * 32], lo[CB_A][2 * 4 * 32];
+  float4 wh[CB_A + CB_B][32];
+  int first[EXPERT_MAX + 1];
+};
+
+int64_t backward_ctas(int64_t n, int n_cells) {
+  const int64_t tiles = (n + CB_ROWS - 1) / CB_ROWS + (n_cells < n ? n_cells : n);
+  const int64_t ctas = (tiles + CB_B - 1) / CB_B;
+  return ctas < CB_SMS ? ctas : CB_SMS;
+}
+
+// c = a b in three products, the small ones first; then c += a b
+__device__ __forceinline__ void mma3_first(float* c, const uint32_t* ah, const uint32_t* al,
+                                           const uint32_t* bh, const uint32_t* bl) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(al[0]), "r"(al[1]), "r"(al[2]), "r"(al[3]), "r"(bh[0]), "r"(bh[1]), "f"(0.0f));
+  mma_tf32(c, ah, bl[0], bl[1]);
+  mma_tf32(c, ah, bh[0], bh[1]);
+}
+__device__ __forceinline__ void mma3(float* c, const uint32_t* ah, const uint32_t* al,
+                                     const uint32_t* bh, const uint32_t* bl) {
+  mma_tf32(c, al, bh[0], bh[1]);
+  mma_tf32(c, ah, bl[0], bl[1]);
+  mma_tf32(c, ah, bh[0], bh[1]);
+}
+// one output channel's gradient carried to a feature of h2 by the heads' weights
+__device__ __forceinline__ float head_grad(const float4& w, const float4& gr) {
+  return fmaf(w.x, gr.x, fmaf(w.y, gr.y, fmaf(w.z, gr.z, w.w * gr.w)));
+}
+
+struct CellsBackwardArgs {
+  const float *x, *d;
+  int64_t n;
+  const int32_t* offset;
+  int n_cells;
+  const float *cell_w, *hidden, *d_raw;
+  float* grad;
+  int* first_out;
+  float *parts_a, *parts_b;
+};
+
+// A role's run over the tiles of one cell: rows begin.., tiles [tile, stop) of it.
+__device__ __forceinline__ void backward_w1(const CellsBackwardArgs& P, CellsBackwardShared& S, int warp,
+                                            int lane, const float* __restrict__ W, int64_t row0,
+                                            int64_t cell_end, int tiles, float* __restrict__ G) {
+  const int g = lane >> 2, t = lane & 3;
+  const float* __restrict__ hidden = P.hidden;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {              // rows of W2^T are h1's features; k step s's columns t, t + 4 are h2's 8t + 2s, + 1
+    const int m = 16 * (q >> 2) + g, f = 8 * t + 2 * (q & 3);
+    uint32_t hi[4], lo[4];
+    split3(__ldg(W + O_W2 + f * 32 + m), hi[0], lo[0]);
+    split3(__ldg(W + O_W2 + f * 32 + m + 8), hi[1], lo[1]);
+    split3(__ldg(W + O_W2 + (f + 1) * 32 + m), hi[2], lo[2]);
+    split3(__ldg(W + O_W2 + (f + 1) * 32 + m + 8), hi[3], lo[3]);
+    S.hi[warp][q * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    S.lo[warp][q * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  __syncwarp();
+  float acc[2][8][4] = {};
+#pragma unroll 1
+  for (; tiles > 0; --tiles, row0 += CB_ROWS) {
+    // g2 as operand B: features 8t .. 8t + 7 of rows g and g + 8; then g1 = (W2^T g2) (h1 > 0)
+    float dz[2][2][4];                       // [rows 0-7, 8-15][m tile]
+    float4 gr[2];
+    float mask[2][8];
+    bool on[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t r = row0 + 8 * q + g;
+      on[q] = r < cell_end;
+      const int64_t rc = on[q] ? r : cell_end - 1;
+      gr[q] = __ldg(reinterpret_cast<const float4*>(P.d_raw) + rc);
+      const float4 m0 = __ldg(reinterpret_cast<const float4*>(hidden) + rc * 16 + 8 + 2 * t);
+      const float4 m1 = __ldg(reinterpret_cast<const float4*>(hidden) + rc * 16 + 9 + 2 * t);
+      mask[q][0] = m0.x, mask[q][1] = m0.y, mask[q][2] = m0.z, mask[q][3] = m0.w;
+      mask[q][4] = m1.x, mask[q][5] = m1.y, mask[q][6] = m1.z, mask[q][7] = m1.w;
+    }
+    float h1[2][4][2], px[2][2][3];          // of rows 8q + 2t + i: the k of the weight products
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t r = min(row0 + 8 * q + 2 * t + i, cell_end - 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h1[q][j][i] = __ldg(hidden + r * 64 + 8 * j + g);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) px[q][i][c] = __ldg(P.x + r * 3 + c);
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float4 w0 = S.wh[warp][8 * t + 2 * s], w1 = S.wh[warp][8 * t + 2 * s + 1];
+      uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        split3(on[q] && mask[q][2 * s] > 0.0f ? head_grad(w0, gr[q]) : 0.0f, bh[q][0], bl[q][0]);
+        split3(on[q] && mask[q][2 * s + 1] > 0.0f ? head_grad(w1, gr[q]) : 0.0f, bh[q][1], bl[q][1]);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint4 hi = S.hi[warp][(m * 4 + s) * 32 + lane], lo = S.lo[warp][(m * 4 + s) * 32 + lane];
+        const uint32_t ahi[4] = {hi.x, hi.y, hi.z, hi.w}, alo[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (s == 0) mma3_first(dz[q][m], ahi, alo, bh[q], bl[q]);
+          else mma3(dz[q][m], ahi, alo, bh[q], bl[q]);
+      }
+    }
+    // C's (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1) are A's (g, t), (g, t+4), (g+8, t), (g+8, t+4)
+    uint32_t zh[2][2][4], zl[2][2][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          split3(h1[q][2 * m + (i >> 1)][i & 1] > 0.0f ? dz[q][m][i] : 0.0f,
+                 zh[q][m][(i & 1) * 2 + (i >> 1)], zl[q][m][(i & 1) * 2 + (i >> 1)]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float e[2][2][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) position_base(px[q][i], 8 * j + g, 1.0f, e[q][i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          split3(e[q][0][i], bh[q][0], bl[q][0]);
+          split3(e[q][1][i], bh[q][1], bl[q][1]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float c[4];
+          mma3_first(c, zh[0][m], zl[0][m], bh[0], bl[0]);
+          mma3(c, zh[1][m], zl[1][m], bh[1], bl[1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][4 * j + i][k] += c[k];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int nn = 16 * m + g + 8 * (k >> 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = position_column(8 * (i >> 2) + 2 * t + (k & 1), i & 3);
+        G[c < 63 ? nn * 63 + c : O_B1 + nn] = acc[m][i][k];
+      }
+    }
+}
+
+__device__ __forceinline__ void backward_w2(const CellsBackwardArgs& P, CellsBackwardShared& S, int warp,
+                                            int lane, int64_t row0, int64_t cell_end, int tiles,
+                                            float* __restrict__ G) {
+  const int g = lane >> 2, t = lane & 3;
+  const float* __restrict__ hidden = P.hidden;
+  float acc[2][4][4] = {}, ah[4][4] = {}, sb2[4] = {};
+#pragma unroll 1
+  for (; tiles > 0; --tiles, row0 += CB_ROWS) {
+    float h1[2][4][2], h2[2][4][2], gc[2][2], dd[2][2][3];
+    float4 gr[2][2];
+    bool on[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t r0 = row0 + 8 * q + 2 * t + i;
+        on[q][i] = r0 < cell_end;
+        const int64_t r = on[q][i] ? r0 : cell_end - 1;
+        gr[q][i] = __ldg(reinterpret_cast<const float4*>(P.d_raw) + r);
+        gc[q][i] = on[q][i] && g < 4 ? __ldg(P.d_raw + r * 4 + (g & 3)) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h1[q][j][i] = __ldg(hidden + r * 64 + 8 * j + g);
+          h2[q][j][i] = __ldg(hidden + r * 64 + 32 + 8 * j + g);
+        }
+#pragma unroll
+        for (int c = 0; c < 3; ++c) dd[q][i][c] = __ldg(P.d + r * 3 + c);
+      }
+    // g2 as operand A: features g + 8 j of rows 8q + 2t + i
+    uint32_t zh[2][2][4], zl[2][2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 w = S.wh[warp][8 * j + g];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float z = on[q][i] && h2[q][j][i] > 0.0f ? head_grad(w, gr[q][i]) : 0.0f;
+          sb2[j] += z;
+          split3(z, zh[q][j >> 1][(j & 1) + 2 * i], zl[q][j >> 1][(j & 1) + 2 * i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        split3(h1[q][j][0], bh[q][0], bl[q][0]);
+        split3(h1[q][j][1], bh[q][1], bl[q][1]);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float c[4];
+        mma3_first(c, zh[0][m], zl[0][m], bh[0], bl[0]);
+        mma3(c, zh[1][m], zl[1][m], bh[1], bl[1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[m][j][k] += c[k];
+      }
+    }
+    // the heads: rows of A are features of [h2 | gamma(d)], columns of B the channels
+    uint32_t gh[2][2], gl[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      split3(gc[q][0], gh[q][0], gl[q][0]);
+      split3(gc[q][1], gh[q][1], gl[q][1]);
+    }
+    // direction base g < 6 (coordinate g / 2, octave 2 (g % 2)): tile 2 its sine and
+    // cosine, tile 3 those of the octave above; rows 6 and 7 hold u0, u1, u2 and 1
+    float v[2][2][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* e = dd[q][i];
+        const float u = (g < 2 || g == 6 ? e[0] : g < 4 || g == 7 ? e[1] : e[2]) / norm3(e);
+        const float u2 = __shfl_sync(0xffffffffu, u, 16 + t);
+        two_octaves(u, 2 * (g & 1), v[q][i]);
+        if (g >= 6) {
+          v[q][i][0] = u;
+          v[q][i][2] = g == 6 ? u2 : 1.0f;
+          v[q][i][1] = v[q][i][3] = 0.0f;
+        }
+      }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      float c[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t fh[4], fl[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            split3(m < 2 ? h2[q][2 * m + k][i] : v[q][i][2 * (m - 2) + k], fh[2 * i + k], fl[2 * i + k]);
+        if (q == 0) mma3_first(c, fh, fl, gh[q], gl[q]);
+        else mma3(c, fh, fl, gh[q], gl[q]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ah[m][k] += c[k];
+    }
+  }
+  G -= O_W2;                                 // by the blob's offsets below
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        G[O_W2 + (16 * m + g + 8 * (k >> 1)) * 32 + 8 * j + 2 * t + (k & 1)] = acc[m][j][k];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float s = sb2[j];
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (t == 0) G[O_B2 + 8 * j + g] = s;
+  }
+  if (t < 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = 2 * t + (k & 1), half = k >> 1;         // channel; row g or g + 8 of the tile
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        G[ch < 3 ? O_WC + ch * 59 + 16 * m + 8 * half + g : O_WS + 16 * m + 8 * half + g] = ah[m][k];
+      const int col = O_WC + ch * 59 + 32;
+      if (ch < 3 && g < 6) {
+        G[col + 3 + 12 * half + 4 * (g >> 1) + 2 * (g & 1)] = ah[2][k];
+        G[col + 3 + 12 * half + 4 * (g >> 1) + 2 * (g & 1) + 1] = ah[3][k];
+      } else if (half == 0) {
+        if (ch < 3 && g >= 6) G[col + g - 6] = ah[2][k];
+        if (ch < 3 && g == 6) G[col + 2] = ah[3][k];
+        if (g == 7) G[ch < 3 ? O_BC + ch : O_BS] = ah[3][k];
+      }
     }
   }
 }
 
-// One CTA per cell; the row's vectors in shared memory, every thread the
-// running sums of its parameters.
-__global__ void __launch_bounds__(CT)
-cells_backward_kernel(const float* __restrict__ x, const float* __restrict__ d, int64_t n,
-                      const int32_t* __restrict__ offset, const float* __restrict__ cell_w,
-                      const float* __restrict__ hidden, const float* __restrict__ d_raw,
-                      float* __restrict__ grad) {
-  // one row: [gamma(x) 63 | 1 | h1 32 | h2 32 | gamma(d) 27] and [g1 32 | g2 32 | g 4]
-  __shared__ float w2[1024], wh[4][32], in[155], out[68];
-  const int cell = blockIdx.x, t = threadIdx.x;
-  const int64_t a = max(offset[cell], 0), b = min((int64_t)offset[cell + 1], n);
-  constexpr int PER = (CELL_NP + CT - 1) / CT;
-  float acc[PER];
-  int ia[PER], ib[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int q = t + j * CT;
-    acc[j] = 0.0f;
-    ia[j] = ib[j] = 0;
-    if (q < O_B1) { ia[j] = q % 63; ib[j] = q / 63; }
-    else if (q < O_W2) { ia[j] = 63; ib[j] = q - O_B1; }
-    else if (q < O_B2) { ia[j] = 64 + (q - O_W2) % 32; ib[j] = 32 + (q - O_W2) / 32; }
-    else if (q < O_WS) { ia[j] = 63; ib[j] = 32 + q - O_B2; }
-    else if (q < O_BS) { ia[j] = 96 + q - O_WS; ib[j] = 67; }
-    else if (q < O_WC) { ia[j] = 63; ib[j] = 67; }
-    else if (q < O_BC) { ia[j] = 96 + (q - O_WC) % 59; ib[j] = 64 + (q - O_WC) / 59; }
-    else if (q < CELL_NP) { ia[j] = 63; ib[j] = 64 + q - O_BC; }
-  }
-  if (a < b) {
-    const float* W = cell_w + (int64_t)cell * CELL_NP;
-    for (int q = t; q < 1024; q += CT) w2[q] = W[O_W2 + q];
-    if (t < 128) wh[t / 32][t & 31] = t < 96 ? W[O_WC + t / 32 * 59 + (t & 31)] : W[O_WS + t - 96];
-  }
-  for (int64_t i = a; i < b; ++i) {
-    __syncthreads();
-    if (t < 63) in[t] = pe_value(x + i * 3, 10, t);
-    else if (t == 63) in[t] = 1.0f;
-    else if (t < 128) in[t] = hidden[i * 64 + t - 64];
-    else if (t < 155) {
-      float u[3];
-      unit3(d + i * 3, u);
-      in[t] = pe_value(u, 4, t - 128);
-    } else if (t >= 160 && t < 164) out[64 + t - 160] = d_raw[i * 4 + t - 160];
-    __syncthreads();
-    if (t < 32) {
-      float s = 0.0f;
-      for (int c = 0; c < 4; ++c) s = fmaf(wh[c][t], out[64 + c], s);
-      out[32 + t] = in[96 + t] > 0.0f ? s : 0.0f;
-      __syncwarp();
-      s = 0.0f;
-      for (int k = 0; k < 32; ++k) s = fmaf(w2[k * 32 + t], out[32 + k], s);
-      out[t] = in[64 + t] > 0.0f ? s : 0.0f;
+// A cell whose tiles all lie in one warp's range is written by that warp; the
+// parts of a cell that spans ranges go to the workspace (slot 0 of a warp: the
+// part at its range's start, slot 1: one that begins inside) and are summed in
+// warp order by cells_join_kernel, so no result depends on timing.
+__global__ void __launch_bounds__(CB_THREADS, 1) cells_backward_kernel(CellsBackwardArgs P) {
+  extern __shared__ __align__(16) uint8_t cells_sm[];
+  CellsBackwardShared& S = *reinterpret_cast<CellsBackwardShared*>(cells_sm);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  tile_prefix<CB_THREADS>(P.offset, P.n, P.n_cells, CB_ROWS, S.first);
+  if (blockIdx.x == 0)
+    for (int c = tid; c <= P.n_cells; c += CB_THREADS) P.first_out[c] = S.first[c];
+  const bool role_a = warp < CB_A;
+  const int W = gridDim.x * (role_a ? CB_A : CB_B);
+  const int w = role_a ? blockIdx.x * CB_A + warp : blockIdx.x * CB_B + warp - CB_A;
+  const int tiles = S.first[P.n_cells], per = (tiles + W - 1) / W;
+  const int begin = (int)min((int64_t)w * per, (int64_t)tiles), end = min(tiles, begin + per);
+  for (int tile = begin; tile < end;) {
+    const int cell = cell_of(S.first, P.n_cells, tile);
+    const int t0 = S.first[cell], t1 = S.first[cell + 1], stop = min(end, max(t1, tile + 1));
+    const float* __restrict__ W2 = P.cell_w + (int64_t)cell * CELL_NP;
+    __syncwarp();                            // the previous cell's fragments are no longer read
+    S.wh[warp][lane] = make_float4(__ldg(W2 + O_WC + lane), __ldg(W2 + O_WC + 59 + lane),
+                                   __ldg(W2 + O_WC + 118 + lane), __ldg(W2 + O_WS + lane));
+    __syncwarp();
+    const int64_t cell_begin = min(max((int64_t)P.offset[cell], (int64_t)0), P.n);
+    const int64_t cell_end = min(max((int64_t)P.offset[cell + 1], (int64_t)0), P.n);
+    const int64_t row0 = cell_begin + (int64_t)max(tile - t0, 0) * CB_ROWS;
+    const bool whole = t0 >= begin && t1 <= end;
+    const int64_t slot = (int64_t)w * 2 + (t0 > begin ? 1 : 0);
+    if (row0 < cell_end) {
+      if (role_a)
+        backward_w1(P, S, warp, lane, W2, row0, cell_end, stop - tile,
+                    whole ? P.grad + (int64_t)cell * CELL_NP : P.parts_a + slot * CB_NA);
+      else
+        backward_w2(P, S, warp, lane, row0, cell_end, stop - tile,
+                    whole ? P.grad + (int64_t)cell * CELL_NP + O_W2 : P.parts_b + slot * CB_NB);
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < PER; ++j) acc[j] = fmaf(in[ia[j]], out[ib[j]], acc[j]);
+    tile = stop;
+  }
+}
+
+// One CTA per cell: nothing where one warp wrote it, zeros where it has no rows,
+// the sum of its parts in warp order where several did; for each role.
+__global__ void __launch_bounds__(256)
+cells_join_kernel(const int* __restrict__ first, int n_cells, int ctas,
+                  const float* __restrict__ parts_a, const float* __restrict__ parts_b,
+                  float* __restrict__ grad) {
+  const int cell = blockIdx.x, t0 = first[cell], t1 = first[cell + 1], tiles = first[n_cells];
+  float* __restrict__ G = grad + (int64_t)cell * CELL_NP;
+  if (t0 >= t1) {
+    for (int q = threadIdx.x; q < CELL_NP; q += 256) G[q] = 0.0f;
+    return;
   }
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (t + j * CT < CELL_NP) grad[(int64_t)cell * CELL_NP + t + j * CT] = acc[j];
+  for (int role = 0; role < 2; ++role) {
+    const int W = ctas * (role ? CB_B : CB_A), per = (tiles + W - 1) / W;
+    const int w0 = t0 / per, w1 = (t1 - 1) / per, N = role ? CB_NB : CB_NA;
+    if (w0 == w1) continue;
+    const float* __restrict__ parts = role ? parts_b : parts_a;
+    float* __restrict__ out = role ? G + O_W2 : G;
+    for (int q = threadIdx.x; q < N; q += 256) {
+      float s = parts[((int64_t)w0 * 2 + (t0 > w0 * per ? 1 : 0)) * N + q];
+#pragma unroll 8
+      for (int w = w0 + 1; w <= w1; ++w) s += parts[(int64_t)w * 2 * N + q];
+      out[q] = s;
+    }
+  }
 }
 
 }  // namespace
@@ -146,16 +726,34 @@ cells_backward_kernel(const float* __restrict__ x, const float* __restrict__ d, 
 cudaError_t launch_cells_forward(const float* x, const float* d, int64_t n, const int32_t* offset,
                                  int n_cells, const float* cell_w, float* raw, float* hidden,
                                  cudaStream_t st) {
-  cells_forward_kernel<<<n_cells, CT, 0, st>>>(x, d, n, offset, cell_w, raw, hidden);
+  const size_t sm = sizeof(CellsForwardShared);
+  cudaError_t e = cudaFuncSetAttribute(cells_forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (n + CF_ROWS - 1) / CF_ROWS + (n_cells < n ? n_cells : n);
+  const unsigned grid = (unsigned)(tiles < 148 * CF_PER_SM ? tiles : 148 * CF_PER_SM);
+  cells_forward_kernel<<<grid, CF_THREADS, sm, st>>>(x, d, n, offset, n_cells, cell_w, raw, hidden);
   return cudaGetLastError();
 }
 
-int64_t cells_backward_workspace(int64_t, int) { return 16; }
+// [first EXPERT_MAX + 1 ints, padded][ctas * CB_A][2][CB_NA], [ctas * CB_B][2][CB_NB] floats
+constexpr int64_t CB_FIRST_BYTES = (EXPERT_MAX + 1 + 3) / 4 * 16;
+int64_t cells_backward_workspace(int64_t n, int n_cells) {
+  return CB_FIRST_BYTES + (backward_ctas(n, n_cells) * 2 * (CB_A * CB_NA + CB_B * CB_NB) * 4 + 15) / 16 * 16;
+}
 
 cudaError_t launch_cells_backward(const float* x, const float* d, int64_t n, const int32_t* offset,
                                   int n_cells, const float* cell_w, const float* hidden,
-                                  const float* d_raw, float* grad, void*, cudaStream_t st) {
-  cells_backward_kernel<<<n_cells, CT, 0, st>>>(x, d, n, offset, cell_w, hidden, d_raw, grad);
+                                  const float* d_raw, float* grad, void* work, cudaStream_t st) {
+  const size_t sm = sizeof(CellsBackwardShared);
+  cudaError_t e = cudaFuncSetAttribute(cells_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  const int ctas = (int)backward_ctas(n, n_cells);
+  int* first = (int*)work;
+  float* parts_a = (float*)((char*)work + CB_FIRST_BYTES);
+  float* parts_b = parts_a + (int64_t)ctas * CB_A * 2 * CB_NA;
+  const CellsBackwardArgs P{x, d, n, offset, n_cells, cell_w, hidden, d_raw, grad, first, parts_a, parts_b};
+  cells_backward_kernel<<<ctas, CB_THREADS, sm, st>>>(P);
+  cells_join_kernel<<<n_cells, 256, 0, st>>>(first, n_cells, ctas, parts_a, parts_b, grad);
   return cudaGetLastError();
 }
 

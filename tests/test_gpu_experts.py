@@ -319,13 +319,16 @@ C3 = 1.25 * 2.0 ** -20      # a product of two operands split in three: lo parts
 
 
 def _encoding_errors(x, d):
-    """Bound on the encodings' errors: sin and cos of the exact angle within 2 steps (2^-23); the unit
-    direction's coordinates within 3.5u of their value, times the angle's slope."""
-    ex = np.concatenate([np.zeros((len(x), 3)), np.full((len(x), 60), 2.0 ** -23)], axis=1)
+    """Bound on the encodings' errors. An even octave's sine and cosine are within e = 2 steps (2^-23) of
+    the angle's; the odd octave above it comes by doubling, 2sc and 1 - 2s^2, whose errors are at most
+    2 (|s| + |c|) e and 4 |s| e (both <= 4e) and one rounding (2^-24). The unit direction's coordinates are
+    within 3.5u of their value, times the angle's slope."""
+    value = np.tile(np.where(np.arange(2) == 0, 1.0, 4.5) * 2.0 ** -23, 15)        # octaves 0, 1, 0, 1, ..
+    ex = np.concatenate([np.zeros((len(x), 3)), np.tile(value, (len(x), 2))], axis=1)
     u = np.abs(d / np.linalg.norm(d, axis=1, keepdims=True))
     slope = np.pi * 2.0 ** np.arange(4)
-    ang = (u[:, :, None] * slope).reshape(len(d), 12) * 3.5 * U
-    return ex, np.concatenate([u * 3.5 * U, ang + 2.0 ** -23, ang + 2.0 ** -23], axis=1)
+    ang = (u[:, :, None] * slope).reshape(len(d), 12) * 3.5 * U + value[:12]
+    return ex, np.concatenate([u * 3.5 * U, ang, ang], axis=1)
 
 
 def _cells_case(torch, seed, counts, extra=0):
