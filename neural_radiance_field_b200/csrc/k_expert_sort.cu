@@ -1,130 +1,277 @@
 // Stable counting sort of (point, expert) pairs by expert.
 //
-// The pairs are cut into one contiguous chunk per warp. A counting pass fills
-// count[chunk][expert]; a column scan turns it into every chunk's first row inside
-// each expert, an expert scan into the experts' offsets; then every warp walks its
-// chunk again in order, 32 pairs at a time. Equal ids among the 32 find each
-// other with a match, a pair's rank among them is the number of lower lanes,
-// and the chunk's running row of the expert advances by their number, so the
-// rows of an expert come in pair order whatever the timing.
+// Up to 1024 pairs: one CTA; a pair's sorted row is the number of kept pairs
+// before it in (expert, pair) order, counted directly (the ids sit in shared
+// memory), and the offsets come from a binary search. One launch.
+//
+// More: three launches over one contiguous chunk of pairs per CTA.
+//   count:   the chunk's pairs of every expert (shared-memory atomics) -> table
+//   columns: for every expert the prefix over the chunks, and its total
+//   place:   the experts' offsets (each CTA scans the totals itself); then, a
+//            tile of the chunk at a time, every warp counts its own run of the
+//            tile (16-bit counters, two experts a word), the counts are scanned
+//            over the warps, and every warp walks its run in order, 32 pairs at
+//            a time. Which of the 32 share an expert comes from one ballot per
+//            bit of the id (12 at most: a third of what a match instruction
+//            costs), a pair's rank among them is the number of lower lanes, and
+//            the expert's counter advances by their number. Rows come out in
+//            pair order whatever the timing.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
 namespace {
 
-constexpr int ES_WARPS = 8;
+constexpr int ES_SMALL = 1024;
+constexpr int ES_WARPS = 16, ES_T = ES_WARPS * 32;
+constexpr int ES_RUN = 4064;                 // pairs of a warp's run in one tile
+constexpr int ES_TILE = ES_WARPS * ES_RUN;
+static_assert(ES_TILE < 65536 && ES_RUN % 32 == 0, "a tile's counts are 16-bit");
+constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
-int64_t sort_chunks(int64_t pairs) {
-  const int64_t most = 148 * ES_WARPS, want = (pairs + 255) / 256;
-  return want < most ? want : most;
+struct SortPlan {
+  int ctas;
+  int64_t chunk;                             // pairs of a CTA, a multiple of ES_T
+};
+// Small tables leave room for three CTAs to an SM; a CTA has 2048 pairs at least,
+// or the tables would outgrow the pairs.
+SortPlan sort_plan(int64_t pairs, int n_experts) {
+  const int64_t most = n_experts <= 1024 ? 148 * 3 : 148, want = (pairs + 2047) / 2048;
+  const int64_t ctas = want < most ? want : most;
+  const int64_t chunk = ((pairs + ctas - 1) / ctas + ES_T - 1) / ES_T * ES_T;
+  return {(int)((pairs + chunk - 1) / chunk), chunk};
 }
 
-__global__ void __launch_bounds__(ES_WARPS * 32)
-es_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int64_t chunks, int n_experts,
-                int32_t* __restrict__ count) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * ES_WARPS + threadIdx.x / 32;
-  if (w >= chunks) return;
-  int32_t* row = count + w * n_experts;
-  for (int e = lane; e < n_experts; e += 32) row[e] = 0;
-  __syncwarp();
-  const int64_t end = min(pairs, (w + 1) * chunk);
-  for (int64_t i0 = w * chunk; i0 < end; i0 += 32) {
-    int id = i0 + lane < end ? ids[i0 + lane] : -1;
-    if ((unsigned)id >= (unsigned)n_experts) id = -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, id);
-    if (id >= 0 && lane == __ffs(peers) - 1) row[id] += __popc(peers);
-    __syncwarp();
+__global__ void __launch_bounds__(ES_SMALL)
+sort_small_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts, int32_t* __restrict__ offset,
+                  int32_t* __restrict__ order, int32_t* __restrict__ pos) {
+  __shared__ __align__(16) int32_t id_s[ES_SMALL];
+  __shared__ int32_t sorted[ES_SMALL];
+  const int t = threadIdx.x, padded = (pairs + 3) & ~3;
+  int id = INT32_MAX;                        // dropped pairs sort behind the kept ones
+  if (t < pairs) {
+    const int v = ids[t];
+    if ((unsigned)v < (unsigned)n_experts) id = v;
   }
-}
-
-__global__ void es_columns_kernel(int32_t* __restrict__ count, int64_t chunks, int n_experts,
-                                  int32_t* __restrict__ offset) {
-  const int e = blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= n_experts) return;
-  int32_t run = 0;
-  for (int64_t w = 0; w < chunks; ++w) {
-    const int32_t c = count[w * n_experts + e];
-    count[w * n_experts + e] = run;
-    run += c;
+  if (t < padded) id_s[t] = id;
+  const int kept = __syncthreads_count(id != INT32_MAX);
+  if (t < pairs) {
+    int row = 0;
+    for (int q = 0; q < padded; q += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(id_s + q);
+      row += (v.x < id || (v.x == id && q < t)) + (v.y < id || (v.y == id && q + 1 < t)) +
+             (v.z < id || (v.z == id && q + 2 < t)) + (v.w < id || (v.w == id && q + 3 < t));
+    }
+    if (id != INT32_MAX) {
+      sorted[row] = id;
+      if (order) order[row] = t;
+    }
+    pos[t] = id != INT32_MAX ? row : -1;
   }
-  offset[e] = run;
-}
-
-__global__ void __launch_bounds__(1024) es_offsets_kernel(int32_t* __restrict__ offset, int n_experts) {
-  __shared__ int32_t sums[1024];
-  const int t = threadIdx.x;
-  int32_t v[4], tot = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = 4 * t + j < n_experts ? offset[4 * t + j] : 0;
-    tot += v[j];
-  }
-  sums[t] = tot;
   __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int32_t u = t >= o ? sums[t - o] : 0;
-    __syncthreads();
-    sums[t] += u;
-    __syncthreads();
+  for (int e = t; e <= n_experts; e += ES_SMALL) {
+    int lo = 0, hi = kept;                   // the first sorted pair of an expert >= e
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < e) lo = mid + 1; else hi = mid;
+    }
+    offset[e] = lo;
   }
-  int32_t run = sums[t] - tot;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (4 * t + j < n_experts) offset[4 * t + j] = run;
-    run += v[j];
-  }
-  if (t == 1023) offset[n_experts] = sums[1023];
 }
 
-__global__ void __launch_bounds__(ES_WARPS * 32)
-es_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int64_t chunks, int n_experts,
-                const int32_t* __restrict__ offset, int32_t* __restrict__ count,
-                int32_t* __restrict__ order, int32_t* __restrict__ pos) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * ES_WARPS + threadIdx.x / 32;
-  if (w >= chunks) return;
-  int32_t* row = count + w * n_experts;
-  const int64_t end = min(pairs, (w + 1) * chunk);
-  for (int64_t i0 = w * chunk; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
-    int id = i < end ? ids[i] : -1;
-    if ((unsigned)id >= (unsigned)n_experts) id = -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, id);
-    const int leader = __ffs(peers) - 1;
-    int base = 0;
-    if (id >= 0 && lane == leader) {
-      base = row[id];
-      row[id] = base + __popc(peers);
-    }
-    base = __shfl_sync(0xffffffffu, base, leader);
-    __syncwarp();
-    if (i < end) {
-      int32_t p = -1;
-      if (id >= 0) {
-        p = offset[id] + base + __popc(peers & ((1u << lane) - 1u));
-        if (order) order[p] = (int32_t)i;
-      }
-      pos[i] = p;
+__global__ void __launch_bounds__(ES_T)
+sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
+                  int32_t* __restrict__ table) {
+  extern __shared__ int32_t hist[];
+  for (int e = threadIdx.x; e < n_experts; e += ES_T) hist[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
+  for (int64_t i = begin + threadIdx.x; i < end; i += 8 * ES_T) {
+    int id[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) id[q] = i + q * ES_T < end ? __ldg(ids + i + q * ES_T) : -1;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if ((unsigned)id[q] < (unsigned)n_experts) atomicAdd(&hist[id[q]], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < n_experts; e += ES_T) table[(int64_t)blockIdx.x * n_experts + e] = hist[e];
+}
+
+// lane = expert, warp = a run of chunks: table becomes the exclusive prefix over
+// the chunks, totals the experts' sums
+__global__ void __launch_bounds__(1024)
+sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int32_t* __restrict__ totals) {
+  __shared__ int32_t part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int per = (chunks + 31) / 32, c0 = min(chunks, warp * per), c1 = min(chunks, c0 + per);
+  int32_t sum = 0;
+  if (e < n_experts)
+    for (int c = c0; c < c1; ++c) sum += table[(int64_t)c * n_experts + e];
+  part[warp][lane] = sum;
+  __syncthreads();
+  int32_t run = 0;
+  for (int w = 0; w < warp; ++w) run += part[w][lane];
+  if (e < n_experts) {
+    if (warp == 31) totals[e] = run + sum;
+    for (int c = c0; c < c1; ++c) {
+      const int32_t v = table[(int64_t)c * n_experts + e];
+      table[(int64_t)c * n_experts + e] = run;
+      run += v;
     }
   }
 }
+
+__global__ void __launch_bounds__(ES_T)
+sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts, int bits,
+                  const int32_t* __restrict__ table, const int32_t* __restrict__ totals,
+                  int32_t* __restrict__ offset, int32_t* __restrict__ order, int32_t* __restrict__ pos) {
+  // base[e]: the next sorted row of expert e for this CTA; words of two 16-bit
+  // counters: [warp][n_experts / 2]
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t sums[ES_WARPS];
+  int32_t* base = sm;
+  const int words = (n_experts + 1) / 2;
+  uint32_t* counts = reinterpret_cast<uint32_t*>(sm + n_experts);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  uint32_t* mine = counts + warp * words;
+  {
+    // exclusive scan of the totals, eight experts a thread
+    int32_t v[8], tot = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 8 * t + j < n_experts ? totals[8 * t + j] : 0;
+      tot += v[j];
+    }
+    int32_t run = tot;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += u;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    run -= tot;
+    for (int w = 0; w < warp; ++w) run += sums[w];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (8 * t + j < n_experts) {
+        base[8 * t + j] = run;
+        if (blockIdx.x == 0) offset[8 * t + j] = run;
+      }
+      run += v[j];
+    }
+    if (blockIdx.x == 0 && t == ES_T - 1) offset[n_experts] = run;
+    __syncthreads();
+    for (int e = t; e < n_experts; e += ES_T) base[e] += table[(int64_t)blockIdx.x * n_experts + e];
+  }
+  const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
+  for (int64_t tile = begin; tile < end; tile += ES_TILE) {
+    const int64_t left = min((int64_t)ES_TILE, end - tile);
+    const int run = (int)((left + ES_WARPS * 32 - 1) / (ES_WARPS * 32)) * 32;   // pairs of a warp
+    const int64_t r0 = tile + (int64_t)warp * run, r1 = min(tile + left, r0 + run);
+    for (int q = lane; q < words; q += 32) mine[q] = 0;
+    __syncwarp();
+    for (int64_t i = r0 + lane; i < r1; i += 256) {
+      int id[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) id[q] = i + 32 * q < r1 ? __ldg(ids + i + 32 * q) : -1;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if ((unsigned)id[q] < (unsigned)n_experts) atomicAdd(&mine[id[q] >> 1], 1u << (16 * (id[q] & 1)));
+    }
+    __syncthreads();
+    // counts -> exclusive prefix over the warps, two experts a word
+    uint32_t all[ES_WORDS];
+#pragma unroll
+    for (int u = 0; u < ES_WORDS; ++u) {
+      const int q = t + u * ES_T;
+      all[u] = 0;
+      if (q < words)
+#pragma unroll
+        for (int w = 0; w < ES_WARPS; ++w) {
+          const uint32_t v = counts[w * words + q];
+          counts[w * words + q] = all[u];
+          all[u] += v;
+        }
+    }
+    __syncthreads();
+    for (int64_t i0 = r0; i0 < r1; i0 += 128) {
+      int id[4];
+      uint32_t peers[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t i = i0 + 32 * q + lane;
+        id[q] = i < r1 ? __ldg(ids + i) : -1;
+        if ((unsigned)id[q] >= (unsigned)n_experts) id[q] = -1;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        peers[q] = __ballot_sync(0xffffffffu, id[q] >= 0);
+        for (int b = 0; b < bits; ++b) {
+          const uint32_t bal = __ballot_sync(0xffffffffu, (id[q] >> b) & 1);
+          peers[q] &= (id[q] >> b) & 1 ? bal : ~bal;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t i = i0 + 32 * q + lane;
+        int32_t p = -1;
+        if (id[q] >= 0) {
+          const int shift = 16 * (id[q] & 1), below = __popc(peers[q] & ((1u << lane) - 1u));
+          p = base[id[q]] + (int32_t)((mine[id[q] >> 1] >> shift) & 0xffffu) + below;
+        }
+        __syncwarp();
+        if (id[q] >= 0) {
+          // one lane a peer group; the word's other expert may have one too, so the add is atomic
+          if ((peers[q] & ((1u << lane) - 1u)) == 0)
+            atomicAdd(&mine[id[q] >> 1], (uint32_t)__popc(peers[q]) << (16 * (id[q] & 1)));
+          if (order) order[p] = (int32_t)i;
+        }
+        if (i < r1) pos[i] = p;
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < ES_WORDS; ++u) {
+      const int q = t + u * ES_T;
+      if (q < words) {
+        base[2 * q] += all[u] & 0xffffu;
+        if (2 * q + 1 < n_experts) base[2 * q + 1] += all[u] >> 16;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+int64_t table_ints(const SortPlan& p, int n_experts) { return (int64_t)p.ctas * n_experts + n_experts; }
 
 }  // namespace
 
 int64_t expert_sort_workspace(int64_t pairs, int n_experts) {
-  return (sort_chunks(pairs) * n_experts * 4 + 15) / 16 * 16;
+  if (pairs <= ES_SMALL) return 16;
+  return (table_ints(sort_plan(pairs, n_experts), n_experts) * 4 + 15) / 16 * 16;
 }
 
 cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts, int32_t* offset,
                                int32_t* order, int32_t* pos, void* work, cudaStream_t st) {
-  const int64_t chunks = sort_chunks(pairs), chunk = (pairs + chunks - 1) / chunks;
-  int32_t* count = (int32_t*)work;
-  const unsigned grid = (unsigned)((chunks + ES_WARPS - 1) / ES_WARPS);
-  es_count_kernel<<<grid, ES_WARPS * 32, 0, st>>>(ids, pairs, chunk, chunks, n_experts, count);
-  es_columns_kernel<<<(n_experts + 63) / 64, 64, 0, st>>>(count, chunks, n_experts, offset);
-  es_offsets_kernel<<<1, 1024, 0, st>>>(offset, n_experts);
-  es_place_kernel<<<grid, ES_WARPS * 32, 0, st>>>(ids, pairs, chunk, chunks, n_experts, offset, count, order, pos);
+  if (pairs <= ES_SMALL) {
+    sort_small_kernel<<<1, ES_SMALL, 0, st>>>(ids, (int)pairs, n_experts, offset, order, pos);
+    return cudaGetLastError();
+  }
+  const SortPlan plan = sort_plan(pairs, n_experts);
+  int32_t* table = (int32_t*)work;
+  int32_t* totals = table + (int64_t)plan.ctas * n_experts;
+  const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
+  cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
+  if (e != cudaSuccess) return e;
+  int bits = 0;
+  while ((1 << bits) < n_experts) ++bits;
+  sort_count_kernel<<<plan.ctas, ES_T, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
+  sort_columns_kernel<<<(n_experts + 31) / 32, 1024, 0, st>>>(table, plan.ctas, n_experts, totals);
+  sort_place_kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, bits, table, totals,
+                                                       offset, order, pos);
   return cudaGetLastError();
 }
 
