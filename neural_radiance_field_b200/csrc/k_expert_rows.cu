@@ -1,86 +1,251 @@
 // Rows taken to the experts' order and back, with weights, and the weights'
-// gradients. One thread per (point, column); the dot products of a weight
-// gradient one warp per pair.
+// gradients:
+//   scatter: rows[pos] = w x, with <x, other[pos]>   (dispatch, combine's backward)
+//   gather:  out = sum_j w rows[pos], with <x, rows[pos]>   (combine, dispatch's backward)
+//
+// Bound by memory: every row is read or written once. A group of 1 to 32 lanes
+// (the power of two that covers a row's vectors) takes one point and holds the
+// point's own row in registers while its k sorted rows pass, so the point's row
+// moves once whatever k is, and the weight gradient comes from the vectors that
+// the row's own pass has in registers. Rows move in 16-byte vectors where their
+// size and both buffers allow it, in 4-byte words where those do, else by
+// element.
 #include "nerf_experts.cuh"
+#include "nerf_vec.cuh"
 
 namespace nerfb {
 namespace {
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f(float v) { return v; }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16(v); }
-template <> __device__ __forceinline__ __half from_f(float v) { return __float2half(v); }
+constexpr int RT = 256;
 
-template <typename T>
-__global__ void scatter_kernel(const T* __restrict__ x, int64_t n, int width,
-                               const int32_t* __restrict__ pos, int k, const float* __restrict__ w,
-                               T* __restrict__ rows) {
-  const int64_t m = n * k;
-  for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < n * width;
-       q += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t i = q / width, c = q - i * width;
-    const float v = to_f(x[q]);
-    for (int j = 0; j < k; ++j) {
-      const int32_t p = pos[i * k + j];
-      if (p >= 0 && p < m) rows[p * (int64_t)width + c] = from_f<T>(w ? w[i * k + j] * v : v);
+// a chunk of at most KC of a point's pairs: sorted rows (-1: none) and weights
+template <int KC>
+struct Pairs {
+  int32_t p[KC];
+  float w[KC];
+  __device__ __forceinline__ void load(const int32_t* __restrict__ pos, const float* __restrict__ weights,
+                                       int64_t i, int k, int j0, int64_t m, bool on) {
+    const int64_t at = i * k + j0;
+    if (KC == 8 && k == 8) {               // 16-byte loads where the caller's buffers have them aligned
+      if ((((uintptr_t)pos | (uintptr_t)weights) & 15) == 0) {
+        const int4 a = on ? __ldg(reinterpret_cast<const int4*>(pos + at)) : make_int4(-1, -1, -1, -1);
+        const int4 b = on ? __ldg(reinterpret_cast<const int4*>(pos + at) + 1) : make_int4(-1, -1, -1, -1);
+        p[0] = a.x, p[1 % KC] = a.y, p[2 % KC] = a.z, p[3 % KC] = a.w;
+        p[4 % KC] = b.x, p[5 % KC] = b.y, p[6 % KC] = b.z, p[7 % KC] = b.w;
+        float4 c = make_float4(1.f, 1.f, 1.f, 1.f), e = c;
+        if (weights && on) {
+          c = __ldg(reinterpret_cast<const float4*>(weights + at));
+          e = __ldg(reinterpret_cast<const float4*>(weights + at) + 1);
+        }
+        w[0] = c.x, w[1 % KC] = c.y, w[2 % KC] = c.z, w[3 % KC] = c.w;
+        w[4 % KC] = e.x, w[5 % KC] = e.y, w[6 % KC] = e.z, w[7 % KC] = e.w;
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if ((uint64_t)(int64_t)p[j] >= (uint64_t)m) p[j] = -1;
+        return;
+      }
     }
-  }
-}
-
-template <typename T>
-__global__ void gather_kernel(const T* __restrict__ rows, int64_t n, int width,
-                              const int32_t* __restrict__ pos, int k, const float* __restrict__ w,
-                              T* __restrict__ out) {
-  const int64_t m = n * k;
-  for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < n * width;
-       q += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t i = q / width, c = q - i * width;
-    float s = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int32_t p = pos[i * k + j];
-      if (p >= 0 && p < m) s = fmaf(w ? w[i * k + j] : 1.0f, to_f(rows[p * (int64_t)width + c]), s);
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      const bool in = on && j0 + j < k;
+      p[j] = in ? __ldg(pos + at + j) : -1;
+      w[j] = in && weights ? __ldg(weights + at + j) : 1.0f;
     }
-    out[q] = from_f<T>(s);
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+      if ((uint64_t)(int64_t)p[j] >= (uint64_t)m) p[j] = -1;
+  }
+};
+
+// dw of a chunk from each lane's partial dot products
+template <int KC>
+__device__ __forceinline__ void store_dots(float* dot, int G, int lane, bool on, int64_t i, int k, int j0,
+                                           float* __restrict__ dw) {
+#pragma unroll
+  for (int j = 0; j < KC; ++j) {
+    if (j0 + j >= k) break;                // uniform over the grid
+    float s = dot[j];
+    for (int o = G >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (on && lane == 0) dw[i * k + j0 + j] = s;
   }
 }
 
-template <typename T>
-__global__ void dots_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t n, int width,
-                            const int32_t* __restrict__ pos, int k, float* __restrict__ dw) {
-  const int64_t m = n * k;
-  const int lane = threadIdx.x & 31;
-  for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32; q < m;
-       q += (int64_t)gridDim.x * blockDim.x / 32) {
-    const int32_t p = pos[q];
-    float s = 0.0f;
-    if (p >= 0 && p < m)
-      for (int c = lane; c < width; c += 32)
-        s = fmaf(to_f(x[q / k * width + c]), to_f(rows[p * (int64_t)width + c]), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) dw[q] = s;
+template <typename T, int BYTES, int KC, bool DW>
+__global__ void __launch_bounds__(RT)
+rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_t n, int nv, int G,
+                    const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
+                    T* __restrict__ rows, float* __restrict__ dw) {
+  using V = Vec<T, BYTES>;
+  using Raw = typename V::Raw;
+  const int lane = threadIdx.x & (G - 1);
+  const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
+  const bool on = i < n;
+  const Raw* xr = reinterpret_cast<const Raw*>(x) + i * nv;
+  for (int j0 = 0; j0 < k; j0 += KC) {
+    Pairs<KC> q;
+    q.load(pos, weights, i, k, j0, m, on);
+    float dot[KC] = {};
+    if (on)
+      for (int v = lane; v < nv; v += G) {
+        V a, b[KC];
+        a.load(xr + v);
+        if (DW) {
+#pragma unroll
+          for (int j = 0; j < KC; ++j)
+            if (q.p[j] >= 0) b[j].load(reinterpret_cast<const Raw*>(other) + (int64_t)q.p[j] * nv + v);
+        }
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          if (q.p[j] < 0) continue;
+          if (DW) {
+#pragma unroll
+            for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a.get(c), b[j].get(c), dot[j]);
+          }
+          if (rows) {
+            V o = a;
+            if (weights) {
+#pragma unroll
+              for (int c = 0; c < V::N; ++c) o.set(c, q.w[j] * a.get(c));
+            }
+            reinterpret_cast<Raw*>(rows)[(int64_t)q.p[j] * nv + v] = o.raw;
+          }
+        }
+      }
+    if (DW) store_dots<KC>(dot, G, lane, on, i, k, j0, dw);
   }
 }
 
-unsigned blocks_for(int64_t threads) {
-  const int64_t b = (threads + 255) / 256;
-  return (unsigned)(b < 148 * 32 ? b : 148 * 32);
+template <typename T, int BYTES, int KC, bool DW>
+__global__ void __launch_bounds__(RT)
+rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t n, int nv, int G,
+                   const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
+                   T* __restrict__ out, float* __restrict__ dw) {
+  using V = Vec<T, BYTES>;
+  using Raw = typename V::Raw;
+  const int lane = threadIdx.x & (G - 1);
+  const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
+  const bool on = i < n;
+  const Raw* rr = reinterpret_cast<const Raw*>(rows);
+  Pairs<KC> q;
+  if (k <= KC) {                             // one pass for the sum and the dot products
+    q.load(pos, weights, i, k, 0, m, on);
+    float dot[KC] = {};
+    if (on)
+      for (int v = lane; v < nv; v += G) {
+        V a, b[KC];
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (q.p[j] >= 0) b[j].load(rr + (int64_t)q.p[j] * nv + v);
+        if (DW) a.load(reinterpret_cast<const Raw*>(x) + i * nv + v);
+        float s[V::N] = {};
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          if (q.p[j] < 0) continue;
+#pragma unroll
+          for (int c = 0; c < V::N; ++c) {
+            const float f = b[j].get(c);
+            s[c] = fmaf(q.w[j], f, s[c]);
+            if (DW) dot[j] = fmaf(a.get(c), f, dot[j]);
+          }
+        }
+        if (out) {
+          V o;
+#pragma unroll
+          for (int c = 0; c < V::N; ++c) o.set(c, s[c]);
+          reinterpret_cast<Raw*>(out)[i * nv + v] = o.raw;
+        }
+      }
+    if (DW) store_dots<KC>(dot, G, lane, on, i, k, 0, dw);
+    return;
+  }
+  if (out && on)                             // more pairs than a chunk: the sum over all of them first
+    for (int v = lane; v < nv; v += G) {
+      float s[V::N] = {};
+      for (int j0 = 0; j0 < k; j0 += KC) {
+        q.load(pos, weights, i, k, j0, m, true);
+        V b[KC];
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (q.p[j] >= 0) b[j].load(rr + (int64_t)q.p[j] * nv + v);
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          if (q.p[j] >= 0) {
+#pragma unroll
+            for (int c = 0; c < V::N; ++c) s[c] = fmaf(q.w[j], b[j].get(c), s[c]);
+          }
+      }
+      V o;
+#pragma unroll
+      for (int c = 0; c < V::N; ++c) o.set(c, s[c]);
+      reinterpret_cast<Raw*>(out)[i * nv + v] = o.raw;
+    }
+  if (DW)
+    for (int j0 = 0; j0 < k; j0 += KC) {
+      q.load(pos, nullptr, i, k, j0, m, on);
+      float dot[KC] = {};
+      if (on)
+        for (int v = lane; v < nv; v += G) {
+          V a;
+          a.load(reinterpret_cast<const Raw*>(x) + i * nv + v);
+#pragma unroll
+          for (int j = 0; j < KC; ++j) {
+            if (q.p[j] < 0) continue;
+            V b;
+            b.load(rr + (int64_t)q.p[j] * nv + v);
+#pragma unroll
+            for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a.get(c), b.get(c), dot[j]);
+          }
+        }
+      store_dots<KC>(dot, G, lane, on, i, k, j0, dw);
+    }
 }
 
-template <typename T>
-void scatter_t(const void* x, const void* other, int64_t n, int width, const int32_t* pos, int k,
-               const float* w, void* rows, float* dw, cudaStream_t st) {
-  if (rows) scatter_kernel<T><<<blocks_for(n * width), 256, 0, st>>>((const T*)x, n, width, pos, k, w, (T*)rows);
-  if (dw) dots_kernel<T><<<blocks_for(n * k * 32), 256, 0, st>>>((const T*)other, (const T*)x, n, width, pos, k, dw);
+struct RowArgs {
+  const void *a, *b;           // scatter: x, other; gather: rows, x
+  int64_t n;
+  int nv, G;
+  const int32_t* pos;
+  int k;
+  const float* w;
+  void* out;                   // scatter: rows; gather: out
+  float* dw;
+  cudaStream_t st;
+};
+
+template <bool SCATTER, typename T, int BYTES, int KC, bool DW>
+void run(const RowArgs& A) {
+  const unsigned grid = (unsigned)((A.n + RT / A.G - 1) / (RT / A.G));
+  if (SCATTER)
+    rows_scatter_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
+                                                                 A.k, A.w, (T*)A.out, A.dw);
+  else
+    rows_gather_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
+                                                                A.k, A.w, (T*)A.out, A.dw);
 }
-template <typename T>
-void gather_t(const void* rows, const void* x, int64_t n, int width, const int32_t* pos, int k,
-              const float* w, void* out, float* dw, cudaStream_t st) {
-  if (out) gather_kernel<T><<<blocks_for(n * width), 256, 0, st>>>((const T*)rows, n, width, pos, k, w, (T*)out);
-  if (dw) dots_kernel<T><<<blocks_for(n * k * 32), 256, 0, st>>>((const T*)rows, (const T*)x, n, width, pos, k, dw);
+// pairs in chunks of two for k <= 2, else of eight: an unused place of a chunk
+// costs its predicates, and a chunk's rows are all in flight at once
+template <bool SCATTER, typename T, int BYTES>
+void run_k(const RowArgs& A) {
+  if (A.k <= 2) A.dw ? run<SCATTER, T, BYTES, 2, true>(A) : run<SCATTER, T, BYTES, 2, false>(A);
+  else A.dw ? run<SCATTER, T, BYTES, 8, true>(A) : run<SCATTER, T, BYTES, 8, false>(A);
+}
+template <bool SCATTER, typename T>
+cudaError_t run_t(RowArgs A, int width) {
+  const uintptr_t all = (uintptr_t)A.a | (uintptr_t)A.b | (uintptr_t)A.out | (uintptr_t)(width * sizeof(T));
+  const int bytes = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)sizeof(T);
+  A.nv = (int)(width * sizeof(T)) / bytes;
+  A.G = 1;
+  while (A.G < A.nv && A.G < 32) A.G *= 2;
+  if (bytes == 16) run_k<SCATTER, T, 16>(A);
+  else if (bytes == 4) run_k<SCATTER, T, 4>(A);
+  else run_k<SCATTER, T, (int)sizeof(T)>(A);
+  return cudaGetLastError();
+}
+template <bool SCATTER>
+cudaError_t run_dtype(const RowArgs& A, int dtype, int width) {
+  if (dtype == NERF_DTYPE_FP32) return run_t<SCATTER, float>(A, width);
+  if (dtype == NERF_DTYPE_BF16) return run_t<SCATTER, __nv_bfloat16>(A, width);
+  return run_t<SCATTER, __half>(A, width);
 }
 
 }  // namespace
@@ -88,19 +253,13 @@ void gather_t(const void* rows, const void* x, int64_t n, int width, const int32
 cudaError_t launch_rows_scatter(const void* x, const void* other, int dtype, int64_t n, int width,
                                 const int32_t* pos, int k, const float* w, void* rows, float* dw,
                                 cudaStream_t st) {
-  if (dtype == NERF_DTYPE_FP32) scatter_t<float>(x, other, n, width, pos, k, w, rows, dw, st);
-  else if (dtype == NERF_DTYPE_BF16) scatter_t<__nv_bfloat16>(x, other, n, width, pos, k, w, rows, dw, st);
-  else scatter_t<__half>(x, other, n, width, pos, k, w, rows, dw, st);
-  return cudaGetLastError();
+  return run_dtype<true>(RowArgs{x, dw ? other : nullptr, n, 0, 0, pos, k, w, rows, dw, st}, dtype, width);
 }
 
 cudaError_t launch_rows_gather(const void* rows, const void* x, int dtype, int64_t n, int width,
                                const int32_t* pos, int k, const float* w, void* out, float* dw,
                                cudaStream_t st) {
-  if (dtype == NERF_DTYPE_FP32) gather_t<float>(rows, x, n, width, pos, k, w, out, dw, st);
-  else if (dtype == NERF_DTYPE_BF16) gather_t<__nv_bfloat16>(rows, x, n, width, pos, k, w, out, dw, st);
-  else gather_t<__half>(rows, x, n, width, pos, k, w, out, dw, st);
-  return cudaGetLastError();
+  return run_dtype<false>(RowArgs{rows, dw ? x : nullptr, n, 0, 0, pos, k, w, out, dw, st}, dtype, width);
 }
 
 }  // namespace nerfb
