@@ -209,14 +209,15 @@ def test_rows_positions_out_of_range_are_dropped(torch):
 # ------------------------------------------------------------------ distillation
 
 def _distill_bounds(s, teacher, ids, T, scale, loss, grad, k):
-    """Worst-case error of (loss, grad in fp32). z = s / T by the rounded 1/T: 2u |z|. The exponent's
-    argument z - m: 2u(|z| + |m|) + u|z - m| <= 6uA, A = max |z|; exp within 2 steps (4u). A sum of the
-    classes in at most classes / 32 + 16 steps. log within 2 steps of its value."""
+    """Worst-case error of (loss, grad in fp32). The exponent's argument (s - m) / T: the difference, the
+    factor (two roundings) and the product, 4u |z - m| <= 8uA with z = s / T and A = max |z|; an exponential
+    within 2^-22 (4u), with 2u for a rescaled running sum. A sum of the classes in at most classes / 32 + 16
+    steps. log within 2 steps of its value."""
     z = s / T
     n, e = s.shape
     fin = np.where(np.isfinite(z), np.abs(z), 0.0)
     A = fin.max(1)
-    d_exp = U * (6 * A + 4)
+    d_exp = U * (8 * A + 6)
     d_sum = d_exp + U * (e / 32 + 16)
     lz = np.log(e) + 2 * A
     d_logq = U * (4 * A + 2 * A) + d_sum + 4 * U * lz + 3 * U * (2 * A + lz)
@@ -286,7 +287,11 @@ def test_distill(torch, n, k, e, dtype, shift):
     alone = torch.full((n,), 7.0, device="cuda")
     nb.nerf_distill_topk(student, *args, alone)
     assert torch.equal(alone, loss)
-    ones = torch.empty_like(grad)
+    other = torch.empty(n * e + 2, device="cuda", dtype=t)[2:].view(n, e)      # aligned unlike the student: same bounds
+    nb.nerf_distill_topk(student, *args, alone, other, _cuda(torch, scale))
+    _near(_np(alone), r_loss, b_loss, "loss, unlike alignment")
+    _near(_np(other), r_grad, (1 + hs) * b_grad + hs * np.abs(r_grad) + TINY[dtype], "grad, unlike alignment")
+    ones = torch.empty_like(gbase)[shift:].view(n, e)
     nb.nerf_distill_topk(student, *args, alone, ones)
     nb.nerf_distill_topk(student, *args, alone, grad, torch.ones(n, device="cuda"))
     assert torch.equal(ones, grad)
@@ -298,15 +303,20 @@ def test_distill_masks_and_extremes(torch, e):
     keep nothing, and rows beside each other that must not mix."""
     import neural_radiance_field_b200 as nb
     low = torch.finfo(torch.float32).min
-    s = torch.zeros(5, e, device="cuda")
+    s = torch.zeros(6, e, device="cuda")
+    s[5] = low                                          # every class masked by it: all alike
     s[0, 1:] = low                                      # all mass on class 0
     s[1, 1:] = float("-inf")
     s[2] = float("nan")
     s[3, 0] = float("-inf")                            # the teacher's only class is ruled out
-    ids = torch.tensor([[0, -1], [0, -1], [-1, -1], [0, -1], [1, 2]], device="cuda", dtype=torch.int32)
-    tl = torch.zeros(5, 2, device="cuda")
-    loss, grad = torch.empty(5, device="cuda"), torch.empty(5, e, device="cuda")
+    ids = torch.tensor([[0, -1], [0, -1], [-1, -1], [0, -1], [1, 2], [1, 2]], device="cuda", dtype=torch.int32)
+    tl = torch.zeros(6, 2, device="cuda")
+    tl[5] = low                                         # the teacher's entries too
+    loss, grad = torch.empty(6, device="cuda"), torch.empty(6, e, device="cuda")
+    nb.nerf_distill_topk(s, tl, ids, 0.5, loss, grad)   # 1 / T > 1: the lowest value times it overflows
+    assert loss[5] == loss[4] and torch.equal(grad[5], grad[4])
     nb.nerf_distill_topk(s, tl, ids, 1.0, loss, grad)
+    assert loss[5] == loss[4] and torch.equal(grad[5], grad[4])
     assert loss[:3].eq(0).all() and grad[:3].eq(0).all()
     assert loss[3] == float("inf") and torch.isfinite(grad[3]).all() and grad[3, 0] == -1
     want = np.log(e) - np.log(2)
