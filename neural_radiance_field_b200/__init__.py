@@ -10,8 +10,9 @@ from __future__ import annotations
 import ctypes
 
 from . import _capi
-from ._capi import (NERF_BF16, NERF_DTYPE_BF16, NERF_DTYPE_FP16, NERF_DTYPE_FP32, NERF_FP32, NERF_TF32, NERF_LAST_1E10, NERF_LAST_TO_FAR, NERF_MODEL_HASHGRID,
-                    NERF_MODEL_KILONERF, NERF_MODEL_MLP, NERF_SIGMA_RELU, NERF_SIGMA_SOFTPLUS,
+from ._capi import (NERF_BF16, NERF_DTYPE_BF16, NERF_DTYPE_FP16, NERF_DTYPE_FP32, NERF_FP32,
+                    NERF_LAST_1E10, NERF_LAST_TO_FAR, NERF_MODEL_HASHGRID, NERF_MODEL_KILONERF,
+                    NERF_MODEL_MLP, NERF_SIGMA_RELU, NERF_SIGMA_SOFTPLUS, NERF_TF32,
                     NerfError, nerf_config, nerf_params)
 
 __all__ = ["Renderer", "nerf_raygen", "nerf_raygen_batch", "nerf_hash_encode_backward",
@@ -124,46 +125,69 @@ def nerf_test_sh(d, out, stream=None):
     _capi.check(_capi.lib().nerf_test_sh(_ptr(d), d.shape[0], _ptr(out), _stream(stream)))
 
 
-def _arg(name, t, dtype, shape):
-    """Pointer of a required tensor argument: a contiguous CUDA tensor of the given
-    type and shape on the current device (the C ABI works on that one)."""
+def _device():
+    """The current device; before CUDA is up no tensor can be on one."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
-    p = _ptr(t)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is {torch.cuda.current_device()}")
-    return p
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
-def _opt(name, t, dtype, shape):
-    return None if t is None else _arg(name, t, dtype, shape)
+def _arg(name, t, dtype, shape, dev):
+    """Address of a tensor argument: contiguous, of the given type and shape, on the
+    current device `dev` (the C ABI works on that one)."""
+    try:
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: expected a CUDA tensor on the current device ({dev}), got one on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name}: expected a CUDA tensor, got {type(t).__name__}") from None
+
+
+def _opt(name, t, dtype, shape, dev):
+    return None if t is None else _arg(name, t, dtype, shape, dev)
+
+
+_DTYPE_CODES = {}
 
 
 def _rows_dtype(name, t):
     """(torch dtype, NERF_DTYPE_*) of a row tensor."""
-    import torch
-    codes = {torch.float32: NERF_DTYPE_FP32, torch.bfloat16: NERF_DTYPE_BF16,
-             torch.float16: NERF_DTYPE_FP16}
-    if not isinstance(t, torch.Tensor) or t.dtype not in codes:
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float32: NERF_DTYPE_FP32, torch.bfloat16: NERF_DTYPE_BF16,
+                             torch.float16: NERF_DTYPE_FP16})
+    code = _DTYPE_CODES.get(getattr(t, "dtype", None))
+    if code is None:
         raise ValueError(f"{name}: expected a float32, bfloat16 or float16 tensor")
-    return t.dtype, codes[t.dtype]
+    return t.dtype, code
 
 
-def _shape(name, t, dims):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name}: expected a tensor of {dims} dimensions")
-    return t.shape
+def _shape2(name, t):
+    """Sizes of a tensor of two dimensions."""
+    s = getattr(t, "shape", ())
+    if len(s) != 2:
+        raise ValueError(f"{name}: expected a tensor of 2 dimensions")
+    return s
 
 
-def _work(t):
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _work(t, dev):
+    if not hasattr(t, "element_size"):
         raise ValueError("workspace: expected a CUDA tensor")
-    return _arg("workspace", t, t.dtype, t.shape), t.numel() * t.element_size()
+    return _arg("workspace", t, t.dtype, t.shape, dev), t.numel() * t.element_size()
+
+
+def _call(fn, *args, stream, dev):
+    """The library call on `stream`, else on the current stream's raw handle (building
+    torch's Stream object for it would take a third of a small call's time)."""
+    import torch
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    lib = _capi._lib or _capi.lib()
+    status = getattr(lib, fn)(*args, s)
+    if status:
+        _capi.check(status)
 
 
 def nerf_expert_sort_workspace(n, k, n_experts):
@@ -177,61 +201,56 @@ def nerf_expert_sort(ids, n_experts, out_offset, out_order, out_pos, workspace, 
     """Stable sort of (point, expert) pairs by expert; ids [n, k] int32, out_order [n * k]
     or None; workspace: any tensor of at least nerf_expert_sort_workspace bytes."""
     import torch
-    n, k = _shape("ids", ids, 2)
-    i32 = torch.int32
-    w, wb = _work(workspace)
-    _capi.check(_capi.lib().nerf_expert_sort(
-        _arg("ids", ids, i32, (n, k)), n, k, int(n_experts),
-        _arg("out_offset", out_offset, i32, (int(n_experts) + 1,)),
-        _opt("out_order", out_order, i32, (n * k,)), _arg("out_pos", out_pos, i32, (n, k)), w, wb,
-        _stream(stream)))
+    n, k = _shape2("ids", ids)
+    i32, dev, e = torch.int32, _device(), int(n_experts)
+    _call("nerf_expert_sort", _arg("ids", ids, i32, (n, k), dev), n, k, e,
+          _arg("out_offset", out_offset, i32, (e + 1,), dev), _opt("out_order", out_order, i32, (n * k,), dev),
+          _arg("out_pos", out_pos, i32, (n, k), dev), *_work(workspace, dev), stream=stream, dev=dev)
 
 
 def nerf_expert_dispatch(x, pos, rows, weights=None, stream=None):
     """rows[pos[i, j]] = weights[i, j] * x[i]; x [n, width], pos [n, k], rows [n * k, width]."""
     import torch
-    (n, c), k = _shape("x", x, 2), _shape("pos", pos, 2)[1]
-    t, code = _rows_dtype("x", x)
-    _capi.check(_capi.lib().nerf_expert_dispatch(
-        _arg("x", x, t, (n, c)), code, n, c, _arg("pos", pos, torch.int32, (n, k)), k,
-        _opt("weights", weights, torch.float32, (n, k)), _arg("rows", rows, t, (n * k, c)),
-        _stream(stream)))
+    (n, c), k = _shape2("x", x), _shape2("pos", pos)[1]
+    (t, code), dev = _rows_dtype("x", x), _device()
+    _call("nerf_expert_dispatch", _arg("x", x, t, (n, c), dev), code, n, c,
+          _arg("pos", pos, torch.int32, (n, k), dev), k,
+          _opt("weights", weights, torch.float32, (n, k), dev), _arg("rows", rows, t, (n * k, c), dev),
+          stream=stream, dev=dev)
 
 
 def nerf_expert_dispatch_backward(d_rows, x, pos, d_x, weights=None, d_weights=None, stream=None):
     """d_x and d_weights of nerf_expert_dispatch (either may be None); see the header."""
     import torch
-    c, (n, k) = _shape("d_rows", d_rows, 2)[1], _shape("pos", pos, 2)
-    t, code = _rows_dtype("d_rows", d_rows)
-    _capi.check(_capi.lib().nerf_expert_dispatch_backward(
-        _arg("d_rows", d_rows, t, (n * k, c)), _opt("x", x, t, (n, c)), code, n, c,
-        _arg("pos", pos, torch.int32, (n, k)), k, _opt("weights", weights, torch.float32, (n, k)),
-        _opt("d_x", d_x, t, (n, c)), _opt("d_weights", d_weights, torch.float32, (n, k)),
-        _stream(stream)))
+    c, (n, k) = _shape2("d_rows", d_rows)[1], _shape2("pos", pos)
+    (t, code), dev, f32 = _rows_dtype("d_rows", d_rows), _device(), torch.float32
+    _call("nerf_expert_dispatch_backward", _arg("d_rows", d_rows, t, (n * k, c), dev),
+          _opt("x", x, t, (n, c), dev), code, n, c, _arg("pos", pos, torch.int32, (n, k), dev), k,
+          _opt("weights", weights, f32, (n, k), dev), _opt("d_x", d_x, t, (n, c), dev),
+          _opt("d_weights", d_weights, f32, (n, k), dev), stream=stream, dev=dev)
 
 
 def nerf_expert_combine(rows, pos, out, weights=None, stream=None):
     """out[i] = sum_j weights[i, j] * rows[pos[i, j]]; rows [n * k, width], out [n, width]."""
     import torch
-    c, (n, k) = _shape("rows", rows, 2)[1], _shape("pos", pos, 2)
-    t, code = _rows_dtype("rows", rows)
-    _capi.check(_capi.lib().nerf_expert_combine(
-        _arg("rows", rows, t, (n * k, c)), code, n, c, _arg("pos", pos, torch.int32, (n, k)), k,
-        _opt("weights", weights, torch.float32, (n, k)), _arg("out", out, t, (n, c)),
-        _stream(stream)))
+    c, (n, k) = _shape2("rows", rows)[1], _shape2("pos", pos)
+    (t, code), dev = _rows_dtype("rows", rows), _device()
+    _call("nerf_expert_combine", _arg("rows", rows, t, (n * k, c), dev), code, n, c,
+          _arg("pos", pos, torch.int32, (n, k), dev), k,
+          _opt("weights", weights, torch.float32, (n, k), dev), _arg("out", out, t, (n, c), dev),
+          stream=stream, dev=dev)
 
 
 def nerf_expert_combine_backward(d_out, rows, pos, d_rows, weights=None, d_weights=None,
                                  stream=None):
     """d_rows and d_weights of nerf_expert_combine (either may be None); see the header."""
     import torch
-    (n, c), k = _shape("d_out", d_out, 2), _shape("pos", pos, 2)[1]
-    t, code = _rows_dtype("d_out", d_out)
-    _capi.check(_capi.lib().nerf_expert_combine_backward(
-        _arg("d_out", d_out, t, (n, c)), _opt("rows", rows, t, (n * k, c)), code, n, c,
-        _arg("pos", pos, torch.int32, (n, k)), k, _opt("weights", weights, torch.float32, (n, k)),
-        _opt("d_rows", d_rows, t, (n * k, c)),
-        _opt("d_weights", d_weights, torch.float32, (n, k)), _stream(stream)))
+    (n, c), k = _shape2("d_out", d_out), _shape2("pos", pos)[1]
+    (t, code), dev, f32 = _rows_dtype("d_out", d_out), _device(), torch.float32
+    _call("nerf_expert_combine_backward", _arg("d_out", d_out, t, (n, c), dev),
+          _opt("rows", rows, t, (n * k, c), dev), code, n, c, _arg("pos", pos, torch.int32, (n, k), dev), k,
+          _opt("weights", weights, f32, (n, k), dev), _opt("d_rows", d_rows, t, (n * k, c), dev),
+          _opt("d_weights", d_weights, f32, (n, k), dev), stream=stream, dev=dev)
 
 
 def nerf_distill_topk(student, teacher_logits, teacher_ids, temperature, out_loss, out_grad=None,
@@ -239,27 +258,24 @@ def nerf_distill_topk(student, teacher_logits, teacher_ids, temperature, out_los
     """Distillation loss [n] (and gradient [n, classes]) of student logits [n, classes]
     against a teacher's kept logits and ids [n, k]; see the header."""
     import torch
-    (n, e), k = _shape("student", student, 2), _shape("teacher_ids", teacher_ids, 2)[1]
-    t, code = _rows_dtype("student", student)
-    f32 = torch.float32
-    _capi.check(_capi.lib().nerf_distill_topk(
-        _arg("student", student, t, (n, e)), code, n, e,
-        _arg("teacher_logits", teacher_logits, f32, (n, k)),
-        _arg("teacher_ids", teacher_ids, torch.int32, (n, k)), k, float(temperature),
-        _opt("row_scale", row_scale, f32, (n,)), _arg("out_loss", out_loss, f32, (n,)),
-        _opt("out_grad", out_grad, t, (n, e)), _stream(stream)))
+    (n, e), k = _shape2("student", student), _shape2("teacher_ids", teacher_ids)[1]
+    (t, code), dev, f32 = _rows_dtype("student", student), _device(), torch.float32
+    _call("nerf_distill_topk", _arg("student", student, t, (n, e), dev), code, n, e,
+          _arg("teacher_logits", teacher_logits, f32, (n, k), dev),
+          _arg("teacher_ids", teacher_ids, torch.int32, (n, k), dev), k, float(temperature),
+          _opt("row_scale", row_scale, f32, (n,), dev), _arg("out_loss", out_loss, f32, (n,), dev),
+          _opt("out_grad", out_grad, t, (n, e), dev), stream=stream, dev=dev)
 
 
 def nerf_cells_forward(x, d, offset, cell_w, out_raw, out_hidden=None, stream=None):
     """Per-cell networks on rows sorted by cell: out_raw [n, 4], out_hidden [n, 64] or None."""
     import torch
-    n, e = _shape("x", x, 2)[0], _shape("cell_w", cell_w, 2)[0]
-    f32 = torch.float32
-    _capi.check(_capi.lib().nerf_cells_forward(
-        _arg("x", x, f32, (n, 3)), _arg("d", d, f32, (n, 3)), n,
-        _arg("offset", offset, torch.int32, (e + 1,)), e, _arg("cell_w", cell_w, f32, (e, 3317)),
-        _arg("out_raw", out_raw, f32, (n, 4)), _opt("out_hidden", out_hidden, f32, (n, 64)),
-        _stream(stream)))
+    n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
+    f32, dev = torch.float32, _device()
+    _call("nerf_cells_forward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
+          _arg("offset", offset, torch.int32, (e + 1,), dev), e,
+          _arg("cell_w", cell_w, f32, (e, 3317), dev), _arg("out_raw", out_raw, f32, (n, 4), dev),
+          _opt("out_hidden", out_hidden, f32, (n, 64), dev), stream=stream, dev=dev)
 
 
 def nerf_cells_backward_workspace(n_rows, n_cells):
@@ -272,14 +288,13 @@ def nerf_cells_backward_workspace(n_rows, n_cells):
 def nerf_cells_backward(x, d, offset, cell_w, hidden, d_raw, grad_cell_w, workspace, stream=None):
     """Weight gradient of nerf_cells_forward (overwritten), from its hidden layers."""
     import torch
-    n, e = _shape("x", x, 2)[0], _shape("cell_w", cell_w, 2)[0]
-    f32 = torch.float32
-    w, wb = _work(workspace)
-    _capi.check(_capi.lib().nerf_cells_backward(
-        _arg("x", x, f32, (n, 3)), _arg("d", d, f32, (n, 3)), n,
-        _arg("offset", offset, torch.int32, (e + 1,)), e, _arg("cell_w", cell_w, f32, (e, 3317)),
-        _arg("hidden", hidden, f32, (n, 64)), _arg("d_raw", d_raw, f32, (n, 4)),
-        _arg("grad_cell_w", grad_cell_w, f32, (e, 3317)), w, wb, _stream(stream)))
+    n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
+    f32, dev = torch.float32, _device()
+    _call("nerf_cells_backward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
+          _arg("offset", offset, torch.int32, (e + 1,), dev), e,
+          _arg("cell_w", cell_w, f32, (e, 3317), dev), _arg("hidden", hidden, f32, (n, 64), dev),
+          _arg("d_raw", d_raw, f32, (n, 4), dev),
+          _arg("grad_cell_w", grad_cell_w, f32, (e, 3317), dev), *_work(workspace, dev), stream=stream, dev=dev)
 
 
 class Renderer:

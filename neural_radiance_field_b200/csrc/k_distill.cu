@@ -5,13 +5,15 @@
 // masks of the type's lowest value must not overflow.)
 //
 // Bound by memory: the logits are read once and the gradient is written once.
-// A row that fits the registers of a warp (rows up to 4 KB) or of a CTA of 256
-// threads (up to 32 KB) stays there between the statistics and the gradient. A
-// longer row is streamed twice, the second time from L2, by a cluster of CTAs
-// that share the row's statistics through distributed shared memory: with few
-// rows the cluster is what fills the GPU, with many it keeps the rows in flight
-// (clusters x row bytes) inside L2. A row's 16-byte vectors start wherever its
-// address allows; up to 14 elements before and after them go one by one.
+// The row stays in registers between its statistics and its gradient, held by a
+// team: a warp (rows up to 16 KB, where there are rows enough to fill the GPU:
+// no barrier anywhere), a CTA of 256 threads (up to 64 KB), or a cluster of two
+// to eight such CTAs (up to 512 KB), which join their statistics through
+// distributed shared memory. Longer rows are streamed twice, the second time
+// from L2, by clusters of eight. Warp 0 of a CTA works out the teacher's
+// probabilities while the row's loads are in flight. A row's 16-byte vectors
+// start wherever its address allows; up to 14 elements before and after them go
+// one by one.
 #include <cooperative_groups.h>
 
 #include "nerf_experts.cuh"
@@ -54,72 +56,83 @@ __device__ __forceinline__ float warp_fold(float v, F f) {
   return v;
 }
 
-// The threads that share a row: a warp, or a CTA of NT threads.
+// (maximum, sum of 2^(c (v - maximum))) of two sets of logits; sums of an empty
+// set or of -inf alone are 0, and no -inf is taken from -inf
+__device__ __forceinline__ float2 join(float2 a, float2 b, float c) {
+  const float m = max_nan(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, 0.0f);
+  return make_float2(m, a.y * exp2_fast((a.x - m) * c) + b.y * exp2_fast((b.x - m) * c));
+}
+__device__ __forceinline__ float2 warp_join(float2 v, float c) {
+  const float m = warp_fold(v.x, [](float a, float b) { return max_nan(a, b); });
+  const float z = m == -INFINITY ? 0.0f : v.y * exp2_fast((v.x - m) * c);
+  return make_float2(m, warp_fold(z, [](float a, float b) { return a + b; }));
+}
+// The whole CTA's (maximum, sum); `red` holds two sets used in turn, so that one
+// barrier a call is enough.
 template <int NT>
-struct Team {
-  float* red;                                // [NT / 32] for a CTA
-  __device__ __forceinline__ int rank() const { return NT == 32 ? threadIdx.x & 31 : threadIdx.x; }
-  __device__ __forceinline__ void sync() const { if (NT == 32) __syncwarp(); else __syncthreads(); }
-  template <typename F>
-  __device__ __forceinline__ float fold(float v, F f) const {
-    v = warp_fold(v, f);
-    if (NT == 32) return v;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int i = 1; i < NT / 32; ++i) v = f(v, red[i]);
-    return v;
-  }
-  __device__ __forceinline__ float max(float v) const { return fold(v, [](float a, float b) { return max_nan(a, b); }); }
-  __device__ __forceinline__ float sum(float v) const { return fold(v, [](float a, float b) { return a + b; }); }
-};
+__device__ __forceinline__ float2 cta_join(float2 v, float c, float2* red) {
+  v = warp_join(v, c);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  constexpr int W = NT / 32;
+  return warp_join((threadIdx.x & 31) < W ? red[threadIdx.x & 31] : make_float2(-INFINITY, 0.0f), c);
+}
 
-// The teacher's side of a row, from its statistics: every thread gets whether an
-// entry is kept; `probs` ([k] of this team) the entries' probabilities.
-template <typename T, int NT>
-__device__ __forceinline__ bool teacher_row(const DistillArgs& A, const Team<NT>& team, int64_t i, const T* s,
-                                            float m, float z, float* probs, bool write_loss) {
+// The teacher's side of a row, by one warp: probabilities of its kept entries
+// (0 for the others) and sum_j p_j log p_j, the same in every lane. `some`: an
+// entry is kept.
+__device__ __forceinline__ float teacher_probs(const DistillArgs& A, int64_t i, float* probs, bool& some) {
+  const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / A.temperature;
   const float* tl = A.tl + i * A.k;
   const int32_t* ti = A.ti + i * A.k;
-  const int r = team.rank();
   auto kept = [&](int j) { return (unsigned)__ldg(ti + j) < (unsigned)A.classes && __ldg(tl + j) != -INFINITY; };
   float top = -INFINITY;
-  for (int j = r; j < A.k; j += NT)
+  for (int j = lane; j < A.k; j += 32)
     if (kept(j)) top = max_nan(top, __ldg(tl + j));
-  top = team.max(top);
-  const bool some = top != -INFINITY;
+  top = warp_fold(top, [](float a, float b) { return max_nan(a, b); });
+  some = top != -INFINITY;
   float norm = 0.0f;
-  for (int j = r; j < A.k; j += NT) {
+  for (int j = lane; j < A.k; j += 32) {
     const float e = kept(j) ? expf((__ldg(tl + j) - top) * inv_t) : 0.0f;
     probs[j] = e;
     norm += e;
   }
-  norm = team.sum(norm);
-  const float log_norm = logf(norm), log_z = logf(z);
+  norm = warp_fold(norm, [](float a, float b) { return a + b; });
+  const float log_norm = logf(norm);
   float l = 0.0f;
-  for (int j = r; j < A.k; j += NT) {
-    const float p = kept(j) ? probs[j] / norm : 0.0f;
+  for (int j = lane; j < A.k; j += 32) {
+    const float p = some ? probs[j] / norm : 0.0f;
     probs[j] = p;
-    if (p != 0.0f)
-      l += p * (((__ldg(tl + j) - top) * inv_t - log_norm) - ((elem_to_f<T>(s[__ldg(ti + j)]) - m) * inv_t - log_z));
+    if (p != 0.0f) l += p * ((__ldg(tl + j) - top) * inv_t - log_norm);
   }
-  l = team.sum(l);
-  if (write_loss && r == 0) A.loss[i] = some ? A.temperature * A.temperature * l : 0.0f;
-  return some;
+  return warp_fold(l, [](float a, float b) { return a + b; });
+}
+
+// The row's loss, by the warp that has its teacher's side.
+template <typename T>
+__device__ __forceinline__ void write_loss(const DistillArgs& A, int64_t i, const T* s, float m, float z,
+                                           const float* probs, float plogp, bool some) {
+  const int lane = threadIdx.x & 31;
+  const float inv_t = 1.0f / A.temperature, log_z = logf(z);
+  const int32_t* ti = A.ti + i * A.k;
+  float l = 0.0f;
+  for (int j = lane; j < A.k; j += 32)
+    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[__ldg(ti + j)]) - m) * inv_t - log_z);
+  l = warp_fold(l, [](float a, float b) { return a + b; });
+  if (lane == 0) A.loss[i] = some ? A.temperature * A.temperature * (plogp - l) : 0.0f;
 }
 
 // The gradient of the kept classes in [lo, hi), which the row's pass wrote as q
 // alone: less the teacher's probability, summed where an id comes twice (its
-// first entry writes).
-template <typename T, int NT>
-__device__ __forceinline__ void kept_gradients(const DistillArgs& A, const Team<NT>& team, int64_t i, const T* s,
+// first entry writes). `r` of `team` threads.
+template <typename T>
+__device__ __forceinline__ void kept_gradients(const DistillArgs& A, int r, int team, int64_t i, const T* s,
                                                T* g, float m, float c, float a, float iz, const float* probs,
                                                int lo, int hi) {
   const int32_t* ti = A.ti + i * A.k;
-  for (int j = team.rank(); j < A.k; j += NT) {
+  for (int j = r; j < A.k; j += team) {
     const int32_t id = __ldg(ti + j);
     if (id < lo || id >= hi) continue;
     float p = 0.0f;
@@ -135,186 +148,241 @@ __device__ __forceinline__ void kept_gradients(const DistillArgs& A, const Team<
 
 constexpr float kLog2e = 1.44269504f;
 
-// Rows in registers: NV vectors a thread (and one single element).
-template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(256)
-distill_rows_kernel(DistillArgs A) {
+// The part of a row that CTA `rank` of `C` holds: vectors [v0, v1) of the row,
+// and single elements (the first CTA those before the vectors, the last those after).
+struct RowPart {
+  int head, v0, v1, lo, hi, single;
+  bool has;
+  template <typename T, int N>
+  static __device__ __forceinline__ RowPart of(const T* s, int classes, int rank, int C, int r) {
+    RowPart p;
+    p.head = N > 1 ? min((int)((0 - (uintptr_t)s) % 16 / sizeof(T)), classes) : 0;
+    const int nv = (classes - p.head) / N;
+    p.v0 = C == 1 ? 0 : (int)((int64_t)nv * rank / C);
+    p.v1 = C == 1 ? nv : (int)((int64_t)nv * (rank + 1) / C);
+    p.lo = rank == 0 ? 0 : p.head + p.v0 * N;
+    p.hi = rank == C - 1 ? classes : p.head + p.v1 * N;
+    const int before = rank == 0 ? p.head : 0, after = rank == C - 1 ? classes - p.head - nv * N : 0;
+    p.single = r < before ? r : p.head + nv * N + r - before;
+    p.has = r < before + after;
+    return p;
+  }
+};
+
+// Rows in registers: NV vectors a thread and one single element. TEAM 32: a warp
+// a row, eight rows to a CTA; TEAM 256: a CTA, or a cluster of them, a row.
+template <typename T, int TEAM, int NV>
+__global__ void __launch_bounds__(256, NV <= 8 ? 3 : TEAM == 32 && NV == 32 ? 1 : 2)
+distill_rows_kernel(DistillArgs A, int C) {
   using V = Vec<T, 16>;
-  constexpr int TEAMS = 256 / NT;
-  __shared__ float red[8], probs_s[TEAMS * DISTILL_MAX_K];
-  const Team<NT> team{red};
-  const int r = team.rank();
-  float* probs = probs_s + (NT == 32 ? threadIdx.x / 32 : 0) * DISTILL_MAX_K;
+  constexpr int TEAMS = 256 / TEAM;
+  __shared__ float2 red[2][8], stat[2];
+  __shared__ float probs_s[TEAMS * DISTILL_MAX_K];
+  __shared__ int some_s[2];
+  const int warp = threadIdx.x >> 5, r = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  float* probs = probs_s + (TEAM == 32 ? warp * DISTILL_MAX_K : 0);
   const float c = kLog2e / A.temperature;
-  for (int64_t i = (int64_t)blockIdx.x * TEAMS + (NT == 32 ? threadIdx.x / 32 : 0); i < A.n;
-       i += (int64_t)gridDim.x * TEAMS) {
+  const int64_t step = (int64_t)gridDim.x / C * TEAMS;
+  int turn = 0;
+  for (int64_t i = (int64_t)blockIdx.x / C * TEAMS + (TEAM == 32 ? warp : 0); i < A.n; i += step, turn ^= 1) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
-    const int head = min((int)((0 - (uintptr_t)s) % 16 / sizeof(T)), A.classes);
-    const int nv = (A.classes - head) / V::N, single = r < head ? r : nv * V::N + r;
-    const bool has = single < A.classes && (r < head || single >= head + nv * V::N);
-    const uint4* sv = reinterpret_cast<const uint4*>(s + head);
+    const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, r);
+    const uint4* sv = reinterpret_cast<const uint4*>(s + P.head) + P.v0 + r;
+    const int nv = P.v1 - P.v0 - r;          // this thread's vectors: q * TEAM < nv
     V v[NV];
-    float one = -INFINITY, m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < NV; ++q)
-      if (r + q * NT < nv) v[q].load(sv + r + q * NT);
-    if (has) one = elem_to_f<T>(s[single]);
-    m = one;
+      if (q * TEAM < nv) v[q].load(sv + q * TEAM);
+    float one = -INFINITY;
+    if (P.has) one = elem_to_f<T>(s[P.single]);
+    bool some = false;
+    float plogp = 0.0f;
+    if (TEAM == 32 || warp == 0) {
+      plogp = teacher_probs(A, i, probs, some);
+      if (TEAM != 32 && r == 0) some_s[turn] = some;
+    }
+    float m = one;
 #pragma unroll
     for (int q = 0; q < NV; ++q)
-      if (r + q * NT < nv)
+      if (q * TEAM < nv)
 #pragma unroll
         for (int e = 0; e < V::N; ++e) m = max_nan(m, v[q].get(e));
-    m = team.max(m);
-    float z = has ? exp2_fast((one - m) * c) : 0.0f;
+    if (TEAM == 32) m = warp_fold(m, [](float a, float b) { return max_nan(a, b); });
+    const float shift = TEAM != 32 && m == -INFINITY ? 0.0f : m;
+    float z = P.has ? exp2_fast((one - shift) * c) : 0.0f;
 #pragma unroll
     for (int q = 0; q < NV; ++q)
-      if (r + q * NT < nv)
+      if (q * TEAM < nv)
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) z += exp2_fast((v[q].get(e) - m) * c);
-    z = team.sum(z);
-    const bool some = teacher_row<T, NT>(A, team, i, s, m, z, probs, true);
+        for (int e = 0; e < V::N; ++e) z += exp2_fast((v[q].get(e) - shift) * c);
+    if (TEAM == 32) {
+      z = warp_fold(z, [](float a, float b) { return a + b; });
+      __syncwarp();
+    } else {
+      float2 all = cta_join<256>(make_float2(m, z), c, red[turn]);
+      if (C > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (r == 0) stat[turn] = all;
+        cluster.sync();
+        all = *cluster.map_shared_rank(&stat[turn], 0);
+        for (int q = 1; q < C; ++q) all = join(all, *cluster.map_shared_rank(&stat[turn], q), c);
+      }
+      m = all.x;
+      z = all.y;
+      some = some_s[turn];
+    }
+    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, plogp, some);
     if (g) {
       const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), iz = 1.0f / z;
-      uint4* gv = reinterpret_cast<uint4*>(g + head);
+      uint4* gv = reinterpret_cast<uint4*>(g + P.head) + P.v0 + r;
+      if (some) {
 #pragma unroll
-      for (int q = 0; q < NV; ++q)
-        if (r + q * NT < nv) {
-          V o;
+        for (int q = 0; q < NV; ++q)
+          if (q * TEAM < nv) {
+            float f[V::N];
 #pragma unroll
-          for (int e = 0; e < V::N; ++e)
-            o.set(e, some ? a * (exp2_fast((v[q].get(e) - m) * c) * iz) : 0.0f);
-          gv[r + q * NT] = o.raw;
-        }
-      if (has) g[single] = elem_from_f<T>(some ? a * (exp2_fast((one - m) * c) * iz) : 0.0f);
-      team.sync();
-      if (some) kept_gradients<T, NT>(A, team, i, s, g, m, c, a, iz, probs, 0, A.classes);
+            for (int e = 0; e < V::N; ++e) f[e] = a * (exp2_fast((v[q].get(e) - m) * c) * iz);
+            V o;
+            o.pack(f);
+            gv[q * TEAM] = o.raw;
+          }
+        if (P.has) g[P.single] = elem_from_f<T>(a * (exp2_fast((one - m) * c) * iz));
+      } else {
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+          if (q * TEAM < nv) gv[q * TEAM] = make_uint4(0, 0, 0, 0);
+        if (P.has) g[P.single] = elem_from_f<T>(0.0f);
+      }
+      if (TEAM == 32) __syncwarp(); else __syncthreads();
+      if (some) kept_gradients<T>(A, r, TEAM, i, s, g, m, c, a, iz, probs, P.lo, P.hi);
     }
-    team.sync();
+    // the next row's probabilities overwrite these
+    if (TEAM == 32) __syncwarp(); else __syncthreads();
   }
+  if (C > 1) cg::this_cluster().sync();      // no CTA ends while another reads its statistics
 }
 
-// Long rows, streamed by clusters: CTA `rank` of a cluster takes the rank-th
-// part of the row's vectors (the last one also the single elements after them,
-// the first one those before).
+// Long rows, or rows whose gradient is aligned unlike them (BYTES = one
+// element), streamed by clusters of CTAs, each a part of the row.
 constexpr int DW_T = 512;
 template <typename T, int BYTES>
 __global__ void __launch_bounds__(DW_T, 2)
-distill_wide_kernel(DistillArgs A) {
+distill_wide_kernel(DistillArgs A, int C) {
   using V = Vec<T, BYTES>;
   using Raw = typename V::Raw;
-  __shared__ float red[DW_T / 32], probs[DISTILL_MAX_K];
-  __shared__ float2 stat;
+  __shared__ float2 red[2][DW_T / 32], stat[2];
+  __shared__ float probs[DISTILL_MAX_K];
+  __shared__ int some_s[2];
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), t = threadIdx.x;
-  const Team<DW_T> team{red};
+  const int rank = C == 1 ? 0 : (int)cluster.block_rank(), t = threadIdx.x, warp = t >> 5;
   const float c = kLog2e / A.temperature;
-  for (int64_t i = blockIdx.x / C; i < A.n; i += gridDim.x / C) {
+  int turn = 0;
+  for (int64_t i = blockIdx.x / C; i < A.n; i += gridDim.x / C, turn ^= 1) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
-    const int head = BYTES == 16 ? min((int)((0 - (uintptr_t)s) % 16 / sizeof(T)), A.classes) : 0;
-    const int nv = (A.classes - head) / V::N;
-    const int v0 = (int)((int64_t)nv * rank / C), v1 = (int)((int64_t)nv * (rank + 1) / C);
-    const int lo = rank == 0 ? 0 : head + v0 * V::N, hi = rank == C - 1 ? A.classes : head + v1 * V::N;
-    const int before = rank == 0 ? head : 0, after = rank == C - 1 ? A.classes - head - nv * V::N : 0;
-    const int single = t < before ? t : head + nv * V::N + t - before;
-    const bool has = t < before + after;
-    const Raw* sv = reinterpret_cast<const Raw*>(s + head);
+    const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
+    const Raw* sv = reinterpret_cast<const Raw*>(s + P.head);
+    bool some = false;
+    float plogp = 0.0f;
+    if (warp == 0) {
+      plogp = teacher_probs(A, i, probs, some);
+      if (t == 0) some_s[turn] = some;
+    }
     // running maximum and sum: the sum is rescaled once per four vectors
-    float m = has ? elem_to_f<T>(s[single]) : -INFINITY, z = has ? 1.0f : 0.0f;
-    for (int q0 = v0 + t; q0 < v1; q0 += 4 * DW_T) {
+    float m = P.has ? elem_to_f<T>(s[P.single]) : -INFINITY, z = P.has && m != -INFINITY ? 1.0f : 0.0f;
+    for (int q0 = P.v0 + t; q0 < P.v1; q0 += 4 * DW_T) {
       V v[4];
       float top = m;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (q0 + u * DW_T < v1) v[u].load(sv + q0 + u * DW_T);
+        if (q0 + u * DW_T < P.v1) v[u].load(sv + q0 + u * DW_T);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (q0 + u * DW_T < v1)
+        if (q0 + u * DW_T < P.v1)
 #pragma unroll
           for (int e = 0; e < V::N; ++e) top = max_nan(top, v[u].get(e));
-      // nothing above -inf yet: any shift does, and -inf - (-inf) must not arise
       const float shift = top == -INFINITY ? 0.0f : top;
       z *= m == -INFINITY ? 0.0f : exp2_fast((m - shift) * c);
       m = top;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (q0 + u * DW_T < v1)
+        if (q0 + u * DW_T < P.v1)
 #pragma unroll
           for (int e = 0; e < V::N; ++e) z += exp2_fast((v[u].get(e) - shift) * c);
     }
-    const float mine = m;
-    m = team.max(m);
-    z = team.sum(mine == -INFINITY ? 0.0f : z * exp2_fast((mine - m) * c));
+    float2 all = cta_join<DW_T>(make_float2(m, z), c, red[turn]);
     if (C > 1) {
-      if (t == 0) stat = make_float2(m, z);
+      if (t == 0) stat[turn] = all;
       cluster.sync();
-      float mm = -INFINITY;
-      for (int q = 0; q < C; ++q) mm = max_nan(mm, cluster.map_shared_rank(&stat, q)->x);
-      float zz = 0.0f;
-      for (int q = 0; q < C; ++q) {
-        const float2 o = *cluster.map_shared_rank(&stat, q);
-        zz += o.x == -INFINITY ? 0.0f : o.y * exp2_fast((o.x - mm) * c);
-      }
-      m = mm;
-      z = zz;
-      cluster.sync();                        // every CTA has read the others' before one writes again or ends
+      all = *cluster.map_shared_rank(&stat[turn], 0);
+      for (int q = 1; q < C; ++q) all = join(all, *cluster.map_shared_rank(&stat[turn], q), c);
     }
-    const bool some = teacher_row<T, DW_T>(A, team, i, s, m, z, probs, rank == 0);
+    m = all.x;
+    z = all.y;
+    some = some_s[turn];
+    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, plogp, some);
     if (g) {
       const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), iz = 1.0f / z;
-      Raw* gv = reinterpret_cast<Raw*>(g + head);
-      for (int q0 = v0 + t; q0 < v1; q0 += 4 * DW_T) {
+      Raw* gv = reinterpret_cast<Raw*>(g + P.head);
+      for (int q0 = P.v0 + t; q0 < P.v1; q0 += 4 * DW_T) {
         V v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (q0 + u * DW_T < v1) v[u].load(sv + q0 + u * DW_T);
+          if (q0 + u * DW_T < P.v1) v[u].load(sv + q0 + u * DW_T);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (q0 + u * DW_T < v1) {
-            V o;
+          if (q0 + u * DW_T < P.v1) {
+            float f[V::N];
 #pragma unroll
             for (int e = 0; e < V::N; ++e)
-              o.set(e, some ? a * (exp2_fast((v[u].get(e) - m) * c) * iz) : 0.0f);
+              f[e] = some ? a * (exp2_fast((v[u].get(e) - m) * c) * iz) : 0.0f;
+            V o;
+            o.pack(f);
             gv[q0 + u * DW_T] = o.raw;
           }
       }
-      if (has) g[single] = elem_from_f<T>(some ? a * (exp2_fast((elem_to_f<T>(s[single]) - m) * c) * iz) : 0.0f);
+      if (P.has) g[P.single] = elem_from_f<T>(some ? a * (exp2_fast((elem_to_f<T>(s[P.single]) - m) * c) * iz) : 0.0f);
       __syncthreads();
-      if (some) kept_gradients<T, DW_T>(A, team, i, s, g, m, c, a, iz, probs, lo, hi);
+      if (some) kept_gradients<T>(A, t, DW_T, i, s, g, m, c, a, iz, probs, P.lo, P.hi);
     }
     __syncthreads();
   }
+  if (C > 1) cluster.sync();
 }
 
-template <typename T, int NT, int NV>
-cudaError_t run_rows(const DistillArgs& A, cudaStream_t st) {
-  const int64_t want = (A.n + 256 / NT - 1) / (256 / NT), most = 148 * 32;
-  distill_rows_kernel<T, NT, NV><<<(unsigned)(want < most ? want : most), 256, 0, st>>>(A);
-  return cudaGetLastError();
-}
-
-template <typename T, int BYTES>
-cudaError_t run_wide(const DistillArgs& A, cudaStream_t st) {
-  // CTAs of a row: as many as fill 148 SMs twice (few rows), and with many rows
-  // enough to keep 296 CTAs' rows within about 32 MB of L2
-  int C = 1;
-  const int64_t bytes = (int64_t)A.classes * sizeof(T);
-  while (C < 8 && bytes / C > 32768 && (A.n * C < 296 || 296 / C * bytes > (32 << 20))) C *= 2;
-  int64_t rows = 296 / C;
-  if (rows > A.n) rows = A.n;
+template <typename K>
+cudaError_t run_clusters(K kernel, const DistillArgs& A, int64_t teams, int threads, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(DW_T);
+  cfg.gridDim = dim3((unsigned)(teams * C));
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, distill_wide_kernel<T, BYTES>, A);
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, A, C);
+}
+
+template <typename T, int TEAM, int NV>
+cudaError_t run_rows(const DistillArgs& A, int C, cudaStream_t st) {
+  constexpr int TEAMS = 256 / TEAM;
+  const int64_t want = (A.n + TEAMS - 1) / TEAMS, most = 148 * 16 / C;
+  return run_clusters(distill_rows_kernel<T, TEAM, NV>, A, want < most ? want : most, 256, C, st);
+}
+
+template <typename T, int BYTES>
+cudaError_t run_wide(const DistillArgs& A, cudaStream_t st) {
+  // CTAs of a row: eight, which with 296 CTAs at a time keeps 37 rows in flight
+  // and their second reading in L2; fewer where a part would be below 32 KB
+  const int64_t bytes = (int64_t)A.classes * sizeof(T);
+  int C = 8;
+  while (C > 1 && bytes / C < 32768) C /= 2;
+  const int64_t most = 296 / C;
+  return run_clusters(distill_wide_kernel<T, BYTES>, A, A.n < most ? A.n : most, DW_T, C, st);
 }
 
 template <typename T>
@@ -322,12 +390,17 @@ cudaError_t run_t(const DistillArgs& A, cudaStream_t st) {
   const int64_t bytes = (int64_t)A.classes * sizeof(T);
   // the vectors of student and gradient rows coincide when both start alike
   if (A.grad && ((uintptr_t)A.grad - (uintptr_t)A.student) % 16) return run_wide<T, (int)sizeof(T)>(A, st);
-  if (bytes <= 512) return run_rows<T, 32, 1>(A, st);
-  if (bytes <= 1024) return run_rows<T, 32, 2>(A, st);
-  if (bytes <= 4096) return run_rows<T, 32, 8>(A, st);
-  if (bytes <= 8192) return run_rows<T, 256, 2>(A, st);
-  if (bytes <= 16384) return run_rows<T, 256, 4>(A, st);
-  if (bytes <= 32768) return run_rows<T, 256, 8>(A, st);
+  if (bytes <= 512) return run_rows<T, 32, 1>(A, 1, st);
+  if (bytes <= 1024) return run_rows<T, 32, 2>(A, 1, st);
+  if (bytes <= 4096) return run_rows<T, 32, 8>(A, 1, st);
+  // a warp a row needs some 1200 rows to fill the SMs
+  if (A.n >= 1184 && bytes <= 8192) return run_rows<T, 32, 16>(A, 1, st);
+  if (A.n >= 1184 && bytes <= 16384) return run_rows<T, 32, 32>(A, 1, st);
+  if (bytes <= 16384) return run_rows<T, 256, 4>(A, 1, st);
+  if (bytes <= 32768) return run_rows<T, 256, 8>(A, 1, st);
+  int C = 1;
+  while (bytes / C > 65536) C *= 2;
+  if (C <= 8) return run_rows<T, 256, 16>(A, C, st);
   return run_wide<T, 16>(A, st);
 }
 

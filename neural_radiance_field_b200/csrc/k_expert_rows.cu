@@ -3,11 +3,13 @@
 //   scatter: rows[pos] = w x, with <x, other[pos]>   (dispatch, combine's backward)
 //   gather:  out = sum_j w rows[pos], with <x, rows[pos]>   (combine, dispatch's backward)
 //
-// Bound by memory: every row is read or written once. A group of 1 to 32 lanes
-// (the power of two that covers a row's vectors) takes one point and holds the
-// point's own row in registers while its k sorted rows pass, so the point's row
-// moves once whatever k is, and the weight gradient comes from the vectors that
-// the row's own pass has in registers. Rows move in 16-byte vectors where their
+// Bound by memory: every row is read or written once. A group of lanes takes one
+// point and holds the point's own row in registers while its k sorted rows pass,
+// so the point's row moves once whatever k is, and the weight gradient comes from
+// the vectors that the row's own pass has in registers. A group is the power of
+// two that covers the row, but no wider than 128 bytes (a full line a step): its
+// lanes then take several vectors of a wide row at once, which keeps more loads
+// in flight and spreads the pair's index work over them. Rows move in 16-byte vectors where their
 // size and both buffers allow it, in 4-byte words where those do, else by
 // element.
 #include "nerf_experts.cuh"
@@ -77,6 +79,7 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
                     T* __restrict__ rows, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
   using Raw = typename V::Raw;
+  constexpr int U = 4;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
   const bool on = i < n;
@@ -86,28 +89,41 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
     q.load(pos, weights, i, k, j0, m, on);
     float dot[KC] = {};
     if (on)
-      for (int v = lane; v < nv; v += G) {
-        V a, b[KC];
-        a.load(xr + v);
-        if (DW) {
+      for (int v0 = lane; v0 < nv; v0 += U * G) {
+        V a[U];
 #pragma unroll
-          for (int j = 0; j < KC; ++j)
-            if (q.p[j] >= 0) b[j].load(reinterpret_cast<const Raw*>(other) + (int64_t)q.p[j] * nv + v);
-        }
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * G < nv) a[u].load(xr + v0 + u * G);
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
           if (q.p[j] < 0) continue;
+          const int64_t row = (int64_t)q.p[j] * nv + v0;
+          V b[U];
           if (DW) {
 #pragma unroll
-            for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a.get(c), b[j].get(c), dot[j]);
+            for (int u = 0; u < U; ++u)
+              if (v0 + u * G < nv) b[u].load(reinterpret_cast<const Raw*>(other) + row + u * G);
           }
           if (rows) {
-            V o = a;
-            if (weights) {
 #pragma unroll
-              for (int c = 0; c < V::N; ++c) o.set(c, q.w[j] * a.get(c));
-            }
-            reinterpret_cast<Raw*>(rows)[(int64_t)q.p[j] * nv + v] = o.raw;
+            for (int u = 0; u < U; ++u)
+              if (v0 + u * G < nv) {
+                V o = a[u];
+                if (weights) {
+                  float f[V::N];
+#pragma unroll
+                  for (int c = 0; c < V::N; ++c) f[c] = q.w[j] * a[u].get(c);
+                  o.pack(f);
+                }
+                reinterpret_cast<Raw*>(rows)[row + u * G] = o.raw;
+              }
+          }
+          if (DW) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (v0 + u * G < nv)
+#pragma unroll
+                for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a[u].get(c), b[u].get(c), dot[j]);
           }
         }
       }
@@ -122,6 +138,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
                    T* __restrict__ out, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
   using Raw = typename V::Raw;
+  constexpr int U = KC == 2 ? 4 : 1;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
   const bool on = i < n;
@@ -131,29 +148,36 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
     q.load(pos, weights, i, k, 0, m, on);
     float dot[KC] = {};
     if (on)
-      for (int v = lane; v < nv; v += G) {
-        V a, b[KC];
+      for (int v0 = lane; v0 < nv; v0 += U * G) {
+        V a[U], b[U][KC];
 #pragma unroll
-        for (int j = 0; j < KC; ++j)
-          if (q.p[j] >= 0) b[j].load(rr + (int64_t)q.p[j] * nv + v);
-        if (DW) a.load(reinterpret_cast<const Raw*>(x) + i * nv + v);
-        float s[V::N] = {};
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * G < nv) {
 #pragma unroll
-        for (int j = 0; j < KC; ++j) {
-          if (q.p[j] < 0) continue;
-#pragma unroll
-          for (int c = 0; c < V::N; ++c) {
-            const float f = b[j].get(c);
-            s[c] = fmaf(q.w[j], f, s[c]);
-            if (DW) dot[j] = fmaf(a.get(c), f, dot[j]);
+            for (int j = 0; j < KC; ++j)
+              if (q.p[j] >= 0) b[u][j].load(rr + (int64_t)q.p[j] * nv + v0 + u * G);
+            if (DW) a[u].load(reinterpret_cast<const Raw*>(x) + i * nv + v0 + u * G);
           }
-        }
-        if (out) {
-          V o;
 #pragma unroll
-          for (int c = 0; c < V::N; ++c) o.set(c, s[c]);
-          reinterpret_cast<Raw*>(out)[i * nv + v] = o.raw;
-        }
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * G < nv) {
+            float s[V::N] = {};
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+              if (q.p[j] < 0) continue;
+#pragma unroll
+              for (int c = 0; c < V::N; ++c) {
+                const float f = b[u][j].get(c);
+                s[c] = fmaf(q.w[j], f, s[c]);
+                if (DW) dot[j] = fmaf(a[u].get(c), f, dot[j]);
+              }
+            }
+            if (out) {
+              V o;
+              o.pack(s);
+              reinterpret_cast<Raw*>(out)[i * nv + v0 + u * G] = o.raw;
+            }
+          }
       }
     if (DW) store_dots<KC>(dot, G, lane, on, i, k, 0, dw);
     return;
@@ -175,8 +199,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
           }
       }
       V o;
-#pragma unroll
-      for (int c = 0; c < V::N; ++c) o.set(c, s[c]);
+      o.pack(s);
       reinterpret_cast<Raw*>(out)[i * nv + v] = o.raw;
     }
   if (DW)
@@ -234,8 +257,9 @@ cudaError_t run_t(RowArgs A, int width) {
   const uintptr_t all = (uintptr_t)A.a | (uintptr_t)A.b | (uintptr_t)A.out | (uintptr_t)(width * sizeof(T));
   const int bytes = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)sizeof(T);
   A.nv = (int)(width * sizeof(T)) / bytes;
+  const int widest = bytes == 16 ? 8 : 32;
   A.G = 1;
-  while (A.G < A.nv && A.G < 32) A.G *= 2;
+  while (A.G < A.nv && A.G < widest) A.G *= 2;
   if (bytes == 16) run_k<SCATTER, T, 16>(A);
   else if (bytes == 4) run_k<SCATTER, T, 4>(A);
   else run_k<SCATTER, T, (int)sizeof(T)>(A);

@@ -241,7 +241,7 @@ def _distill_bounds(s, teacher, ids, T, scale, loss, grad, k):
 
 
 DISTILL = [(1, 1, 1), (1, 8, 4096), (5, 3, 2), (33, 8, 31), (64, 16, 100), (17, 5, 333), (9, 32, 1024), (20, 16, 4096),
-           (7, 256, 5000), (6, 9, 8191), (4, 32, 20001), (3, 40, 100003), (2, 7, 262144), (300, 2, 64)]
+           (1300, 8, 4096), (1201, 3, 1501), (7, 256, 5000), (6, 9, 8191), (4, 32, 20001), (3, 40, 100003), (2, 7, 262144), (300, 2, 64)]
 
 
 @pytest.mark.parametrize("n,k,e", DISTILL)
