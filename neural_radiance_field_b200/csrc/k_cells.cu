@@ -17,7 +17,7 @@
 // columns 2t, 2t + 1. An angle's sine and cosine are a pair of fragment columns,
 // and the columns are ordered so that a lane that has an even octave has the odd
 // one above it too: sin 2a = 2 sin a cos a and cos 2a = 1 - 2 sin^2 a, four
-// operations in place of a second sincospif (about 35). With base q = 0..14
+// operations in place of a second evaluation. With base q = 0..14
 // (coordinate q / 5, octave 2 (q % 5)), base 15 stands for x, y, z and a constant.
 #include "nerf_experts.cuh"
 
@@ -25,7 +25,7 @@ namespace nerfb {
 namespace {
 
 // parameter offsets inside a cell's blob
-constexpr int O_W1 = 0, O_B1 = 2016, O_W2 = 2048, O_B2 = 3072, O_WS = 3104, O_BS = 3136, O_WC = 3137,
+constexpr int O_B1 = 2016, O_W2 = 2048, O_B2 = 3072, O_WS = 3104, O_BS = 3136, O_WC = 3137,
               O_BC = 3314;
 
 __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -40,34 +40,84 @@ __device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(__fsub_rn(v, __uint_as_float(hi)));
 }
-// 1 / |d| as the divisor's reciprocal is not taken: each coordinate needed is
-// divided once by the rounded norm.
-__device__ __forceinline__ float norm3(const float* d) {
-  return sqrtf(fmaf(d[0], d[0], fmaf(d[1], d[1], d[2] * d[2])));
+__device__ __noinline__ float2 sincos_pi_far(float v) {
+  float2 r;
+  sincospif(v, &r.x, &r.y);
+  return r;
 }
-// v = (sin, cos) of octave k of coordinate xc, then of octave k + 1
-__device__ __forceinline__ void two_octaves(float xc, int k, float* v) {
-  sincospif(xc * __int_as_float((127 + k) << 23), v, v + 1);
+// sin and cos of pi v: v = n / 2 + r exactly, |r| <= 1/4, and two polynomials in
+// r^2 whose coefficients were fitted to sin(pi r) / r and cos(pi r) on that
+// interval by reweighted least squares. Within 1.5 * 2^-24 of the value over
+// |v| <= 384; 20 operations, two fifths fewer than the library call.
+__device__ __forceinline__ void sincos_pi(float v, float* s, float* c) {
+  if (fabsf(v) > 1048576.0f) {               // the quadrant would not fit the mantissa
+    const float2 f = sincos_pi_far(v);
+    *s = f.x;
+    *c = f.y;
+    return;
+  }
+  const float t = fmaf(v, 2.0f, 12582912.0f);
+  const unsigned n = __float_as_uint(t);
+  const float r = fmaf(t - 12582912.0f, -0.5f, v), q = r * r;
+  const float a = r * fmaf(fmaf(fmaf(-5.890786648e-01f, q, 2.549767256f), q, -5.167707920f), q, 3.141592741f);
+  const float b = fmaf(fmaf(fmaf(fmaf(2.314295471e-01f, q, -1.335058451f), q, 4.058707905f), q, -4.934802055f), q, 1.0f);
+  const float p = n & 1 ? b : a, o = n & 1 ? a : b;
+  *s = __uint_as_float(__float_as_uint(p) ^ ((n << 30) & 0x80000000u));
+  *c = __uint_as_float(__float_as_uint(o) ^ (((n + 1) << 30) & 0x80000000u));
+}
+// the unit direction: each coordinate divided by the rounded norm
+__device__ __forceinline__ void unit3(float* d) {
+  const float len = sqrtf(fmaf(d[0], d[0], fmaf(d[1], d[1], d[2] * d[2])));
+  d[0] /= len;
+  d[1] /= len;
+  d[2] /= len;
+}
+// v = (sin, cos) of octave k of coordinate xc, then of octave k + 1; scale = 2^k
+__device__ __forceinline__ void two_octaves(float xc, float scale, float* v) {
+  sincos_pi(xc * scale, v, v + 1);
   const float s2 = v[0] + v[0];
   v[2] = s2 * v[1];
   v[3] = fmaf(-s2, v[0], 1.0f);
 }
-// base q of the position encoding: (sin, cos) of two octaves, or x, y, z, one
-__device__ __forceinline__ void position_base(const float* x, int q, float one, float* v) {
-  const int c = (q >= 5) + (q >= 10), k = 2 * (q - 5 * c);
-  two_octaves(c == 0 ? x[0] : c == 1 ? x[1] : x[2], k & 15, v);
-  if (q == 15) {
-    v[0] = x[0];
-    v[1] = x[1];
-    v[2] = x[2];
-    v[3] = one;
+// a lane's base of the position encoding: coordinate and 2^octave
+struct Base {
+  int c;
+  float scale;
+  bool last;                                 // base 15: x, y, z, constant
+  __device__ __forceinline__ explicit Base(int q) {
+    c = (q >= 5) + (q >= 10);
+    scale = __int_as_float((127 + 2 * (q - 5 * c)) << 23);
+    last = q == 15;
   }
-}
+  // (sin, cos) of two octaves of the row x, or x, y, z, one
+  __device__ __forceinline__ void encode(const float* x, float one, float* v) const {
+    two_octaves(x[c], scale, v);
+    if (last) {
+      v[0] = x[0];
+      v[1] = x[1];
+      v[2] = x[2];
+      v[3] = one;
+    }
+  }
+};
 // column of gamma(x) that entry i (sin, cos, sin, cos) of base q stands for; 63 the constant
 __device__ __forceinline__ int position_column(int q, int i) {
   const int c = (q >= 5) + (q >= 10), k = 2 * (q - 5 * c) + (i >> 1);
   return q < 15 ? 3 + 30 * (i & 1) + 10 * c + k : i < 3 ? i : 63;
 }
+
+// Asynchronous copies into shared memory; zeros where `in` is false.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // first[c] = tiles of `rows` rows of the cells before c, first[n_cells] = all of
 // them: each warp scans a run of cells, 32 at a time. Offsets are taken into
@@ -127,12 +177,14 @@ __device__ __forceinline__ int cell_of(const int* first, int n_cells, int tile) 
 
 constexpr int CF_WARPS = 4, CF_THREADS = CF_WARPS * 32;
 constexpr int CF_ROWS = CF_WARPS * 32;       // rows of a tile, 32 per warp
-constexpr int CF_PER_SM = 4;
+constexpr int CF_PER_SM = 4;                 // resident CTAs
+constexpr int CF_WAVES = 3;                  // CTAs of the grid per resident one
 struct CellsForwardShared {
   float4 w1[8 * 4 * 32];      // B fragments of W1: [k step][n tile][lane] = (hi, hi, lo, lo)
   float4 w2[4 * 4 * 32];
   float4 wh[32], wd[27], bh;  // heads (r, g, b, sigma) on h2 and (r, g, b, 0) on gamma(d)
   float b1[32], b2[32];
+  float rows[CF_WARPS][2][2][96];             // [warp][stage]: x and d of a warp's 32 rows
   int first[EXPERT_MAX + 1];
 };
 
@@ -141,6 +193,26 @@ __device__ __forceinline__ float4 b_fragment(float b0, float b1) {
   split3(b0, h0, l0);
   split3(b1, h1, l1);
   return make_float4(__uint_as_float(h0), __uint_as_float(h1), __uint_as_float(l0), __uint_as_float(l1));
+}
+
+// One k step of a layer: 32 rows (two fragments) x 32 outputs (four). The three
+// products of an accumulator are eight instructions apart.
+__device__ __forceinline__ void layer_step(float (&c)[2][4][4], const uint32_t (&ah)[2][4],
+                                           const uint32_t (&al)[2][4], const float4* w) {
+  uint32_t bh[4][2], bl[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = w[j * 32];
+    bh[j][0] = __float_as_uint(v.x), bh[j][1] = __float_as_uint(v.y);
+    bl[j][0] = __float_as_uint(v.z), bl[j][1] = __float_as_uint(v.w);
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        mma_tf32(c[m][j], p == 0 ? al[m] : ah[m], p == 1 ? bl[j][0] : bh[j][0], p == 1 ? bl[j][1] : bh[j][1]);
 }
 
 __global__ void __launch_bounds__(CF_THREADS, CF_PER_SM)
@@ -154,9 +226,40 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
   tile_prefix<CF_THREADS>(offset, n, n_cells, CF_ROWS, S.first);
   const int tiles = S.first[n_cells], per = (tiles + gridDim.x - 1) / gridDim.x;
   const int end = min(tiles, (int)(blockIdx.x + 1) * per);
-  int staged = -1;
-  for (int tile = blockIdx.x * per; tile < end; ++tile) {
-    const int cell = cell_of(S.first, n_cells, tile);
+  // A tile's cell and this warp's rows of it, found one tile ahead; its positions
+  // and directions are on their way from then on.
+  struct Tile {
+    int cell;
+    int64_t row0;
+    int rows;                                // 0 or less: none for this warp
+  } now{-1, 0, 0}, next{-1, 0, 0};
+  auto look = [&](int tile, int stage, Tile before) {
+    Tile n_{before.cell, 0, 0};
+    if (tile < end) {
+      if (n_.cell < 0 || tile >= S.first[n_.cell + 1]) n_.cell = cell_of(S.first, n_cells, tile);
+      const int64_t lo = min(max((int64_t)__ldg(offset + n_.cell), (int64_t)0), n);
+      const int64_t hi = min(max((int64_t)__ldg(offset + n_.cell + 1), (int64_t)0), n);
+      n_.row0 = lo + (int64_t)max(tile - S.first[n_.cell], 0) * CF_ROWS + warp * 32;
+      n_.rows = (int)min((int64_t)32, hi - n_.row0);
+      const int have = max(n_.rows, 0) * 3;
+      const int64_t at = have > 0 ? n_.row0 * 3 : 0;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int e = 32 * q + lane;
+        copy_async4(&S.rows[warp][stage][0][e], x + at + (e < have ? e : 0), e < have);
+        copy_async4(&S.rows[warp][stage][1][e], d + at + (e < have ? e : 0), e < have);
+      }
+    }
+    copy_commit();
+    return n_;
+  };
+  int staged = -1, stage = 0;
+  next = look(blockIdx.x * per, 0, now);
+  for (int tile = blockIdx.x * per; tile < end; ++tile, stage ^= 1) {
+    now = next;
+    __syncwarp();                            // the stage's readers, a tile ago, are done
+    next = look(tile + 1, stage ^ 1, now);
+    const int cell = now.cell;
     if (cell != staged) {
       staged = cell;
       __syncthreads();                       // the previous cell's weights are no longer read
@@ -189,19 +292,14 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
       }
       __syncthreads();
     }
+    if (now.rows <= 0) continue;
+    copy_wait<1>();                          // this tile's copies; the next tile's may still run
+    __syncwarp();
     // this warp's 32 rows: lane (g, t) works on rows g + 8 r, r = 0..3
-    const int64_t cell_begin = min(max((int64_t)offset[cell], (int64_t)0), n);
-    const int64_t cell_end = min(max((int64_t)offset[cell + 1], (int64_t)0), n);
-    const int64_t row0 = cell_begin + (int64_t)max(tile - S.first[cell], 0) * CF_ROWS + warp * 32;
-    if (row0 >= cell_end) continue;
-    int64_t row[4];
-    float px[4][3];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      row[r] = min(row0 + g + 8 * r, cell_end - 1);
-#pragma unroll
-      for (int c = 0; c < 3; ++c) px[r][c] = x[row[r] * 3 + c];
-    }
+    const float* xs = S.rows[warp][stage][0];
+    float* ds = S.rows[warp][stage][1];
+    const int64_t row0 = now.row0;
+    const int rows = now.rows;
     float h[2][4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -217,28 +315,17 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       uint32_t ah[2][2][4], al[2][2][4];
+      const Base base(4 * b + t);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float v[4];
-        position_base(px[r], 4 * b + t, 0.0f, v);
+        base.encode(xs + 3 * (g + 8 * r), 0.0f, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           split3(v[i], ah[i >> 1][r >> 1][2 * (i & 1) + (r & 1)], al[i >> 1][r >> 1][2 * (i & 1) + (r & 1)]);
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 w = S.w1[((2 * b + s) * 4 + j) * 32 + lane];
-          const uint32_t bh0 = __float_as_uint(w.x), bh1 = __float_as_uint(w.y),
-                         bl0 = __float_as_uint(w.z), bl1 = __float_as_uint(w.w);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            mma_tf32(h[m][j], al[s][m], bh0, bh1);
-            mma_tf32(h[m][j], ah[s][m], bl0, bl1);
-            mma_tf32(h[m][j], ah[s][m], bh0, bh1);
-          }
-        }
+      for (int s = 0; s < 2; ++s) layer_step(h, ah[s], al[s], &S.w1[(2 * b + s) * 128 + lane]);
     }
     float h2[2][4][4];
 #pragma unroll
@@ -253,8 +340,8 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
         if (hidden) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (row0 + g + 8 * (2 * m + i) < cell_end)
-              *reinterpret_cast<float2*>(hidden + row[2 * m + i] * 64 + 8 * j + 2 * t) =
+            if (g + 8 * (2 * m + i) < rows)
+              *reinterpret_cast<float2*>(hidden + (row0 + g + 8 * (2 * m + i)) * 64 + 8 * j + 2 * t) =
                   make_float2(h[m][j][2 * i], h[m][j][2 * i + 1]);
         }
       }
@@ -268,18 +355,7 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3(h[m][s][i], ah[m][(i & 1) * 2 + (i >> 1)], al[m][(i & 1) * 2 + (i >> 1)]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = S.w2[(s * 4 + j) * 32 + lane];
-        const uint32_t bh0 = __float_as_uint(w.x), bh1 = __float_as_uint(w.y),
-                       bl0 = __float_as_uint(w.z), bl1 = __float_as_uint(w.w);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_tf32(h2[m][j], al[m], bh0, bh1);
-          mma_tf32(h2[m][j], ah[m], bl0, bl1);
-          mma_tf32(h2[m][j], ah[m], bh0, bh1);
-        }
-      }
+      layer_step(h2, ah, al, &S.w2[s * 128 + lane]);
     }
     // the heads on the FMA pipe, which the tensor products leave idle: each lane
     // its eight features of h2 and its share of gamma(d), for four rows
@@ -290,22 +366,24 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float a = fmaxf(h2[r >> 1][j][2 * (r & 1)], 0.0f), b = fmaxf(h2[r >> 1][j][2 * (r & 1) + 1], 0.0f);
-        if (hidden && row0 + g + 8 * r < cell_end)
-          *reinterpret_cast<float2*>(hidden + row[r] * 64 + 32 + 8 * j + 2 * t) = make_float2(a, b);
+        if (hidden && g + 8 * r < rows)
+          *reinterpret_cast<float2*>(hidden + (row0 + g + 8 * r) * 64 + 32 + 8 * j + 2 * t) = make_float2(a, b);
         o[r][0] = fmaf(w0.x, a, fmaf(w1.x, b, o[r][0]));
         o[r][1] = fmaf(w0.y, a, fmaf(w1.y, b, o[r][1]));
         o[r][2] = fmaf(w0.z, a, fmaf(w1.z, b, o[r][2]));
         o[r][3] = fmaf(w0.w, a, fmaf(w1.w, b, o[r][3]));
       }
     }
-    // lane t < 3 has coordinate t of the direction and its four octaves
+    // one lane a row makes its direction a unit vector; then lane t < 3 has
+    // coordinate t and its four octaves
+    unit3(ds + 3 * lane);
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float dd[3] = {d[row[r] * 3], d[row[r] * 3 + 1], d[row[r] * 3 + 2]};
-      const float ut = (t == 0 ? dd[0] : t == 1 ? dd[1] : dd[2]) / norm3(dd);
+      const float ut = ds[3 * (g + 8 * r) + min(t, 2)];
       float v[8];
-      two_octaves(ut, 0, v);
-      two_octaves(ut, 2, v + 4);
+      two_octaves(ut, 1.0f, v);
+      two_octaves(ut, 4.0f, v + 4);
       if (t < 3) {
         const float4 wu = S.wd[t];
         o[r][0] = fmaf(wu.x, ut, o[r][0]);
@@ -333,10 +411,11 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
       vp[c] = (odd ? p1 : p0) + __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
     }
     const float4 bh = S.bh;
-    if (row0 + g + 8 * t < cell_end)
+    if (g + 8 * t < rows)
       reinterpret_cast<float4*>(raw)[row0 + g + 8 * t] =
           make_float4(v.x + bh.x, v.y + bh.y, v.z + bh.z, v.w + bh.w);
   }
+  copy_wait<0>();
 }
 
 // ------------------------------------------------------------------ backward
@@ -350,12 +429,21 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
 // with the number of additions and all in one direction (2e-6 of the gradient
 // at 370 rows a cell); so a tile's products go to a fresh accumulator, which is
 // added to the cell's by a rounded addition.
-constexpr int CB_A = 8, CB_B = 4;             // warps of each role in a CTA
+constexpr int CB_A = 6, CB_B = 6;             // warps of each role in a CTA (measured: 8 and 4 297 us, 7 and 5 260, 6 and 6 241)
 constexpr int CB_THREADS = (CB_A + CB_B) * 32;
 constexpr int CB_ROWS = 16;
 constexpr int CB_SMS = 148;
 constexpr int CB_NA = O_W2, CB_NB = CELL_NP - O_W2;   // parameters of each role
+// What a tile's rows need, brought in by asynchronous copies one tile ahead of
+// its use. A hidden row takes 68 floats: fragments read rows 2t apart in one
+// access, and 8t + g then falls in 32 different banks.
+struct BackwardTile {
+  float hidden[CB_ROWS][68];
+  float4 d_raw[CB_ROWS];
+  float v[CB_ROWS * 3];                       // x (first role) or d (second)
+};
 struct CellsBackwardShared {
+  BackwardTile tile[CB_A + CB_B][2];
   // A fragments of W2^T, [m tile][k step][lane], hi and lo; heads (r, g, b, sigma) on h2
   uint4 hi[CB_A][2 * 4 * 32], lo[CB_A][2 * 4 * 32];
   float4 wh[CB_A + CB_B][32];
@@ -368,25 +456,57 @@ int64_t backward_ctas(int64_t n, int n_cells) {
   return ctas < CB_SMS ? ctas : CB_SMS;
 }
 
-// c = a b in three products, the small ones first; then c += a b
-__device__ __forceinline__ void mma3_first(float* c, const uint32_t* ah, const uint32_t* al,
-                                           const uint32_t* bh, const uint32_t* bl) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(al[0]), "r"(al[1]), "r"(al[2]), "r"(al[3]), "r"(bh[0]), "r"(bh[1]), "f"(0.0f));
-  mma_tf32(c, ah, bl[0], bl[1]);
-  mma_tf32(c, ah, bh[0], bh[1]);
-}
-__device__ __forceinline__ void mma3(float* c, const uint32_t* ah, const uint32_t* al,
-                                     const uint32_t* bh, const uint32_t* bl) {
-  mma_tf32(c, al, bh[0], bh[1]);
-  mma_tf32(c, ah, bl[0], bl[1]);
-  mma_tf32(c, ah, bh[0], bh[1]);
+// c += a b, or c = a b where `first`
+__device__ __forceinline__ void mma_from(bool first, float* c, const uint32_t* a, const uint32_t* b) {
+  if (first)
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
+  else
+    mma_tf32(c, a, b[0], b[1]);
 }
 // one output channel's gradient carried to a feature of h2 by the heads' weights
 __device__ __forceinline__ float head_grad(const float4& w, const float4& gr) {
   return fmaf(w.x, gr.x, fmaf(w.y, gr.y, fmaf(w.z, gr.z, w.w * gr.w)));
+}
+
+// One group of copies: rows row0 .. row0 + 15; zeros for a row past the cell's
+// end, which then has no gradient and no input.
+__device__ __forceinline__ void fetch_tile(BackwardTile& T, int lane, const float* __restrict__ hidden,
+                                           const float* __restrict__ d_raw, const float* __restrict__ v,
+                                           int64_t row0, int64_t cell_end) {
+  const int64_t safe = min(row0, cell_end - 1);
+  const int rows = (int)min((int64_t)CB_ROWS, cell_end - row0);      // 0 or less: nothing is read
+  const float* h = hidden + safe * 64;
+  const bool full = rows == CB_ROWS;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int r = 2 * q + (lane >> 4);
+    const bool in = full || r < rows;
+    copy_async16(&T.hidden[r][(lane & 15) * 4], h + (in ? r * 64 + (lane & 15) * 4 : 0), in);
+  }
+  if (lane < 16) copy_async16(&T.d_raw[lane], d_raw + (safe + (lane < rows ? lane : 0)) * 4, lane < rows);
+  const float* w = v + safe * 3;
+  copy_async4(&T.v[lane], w + (lane < 3 * rows ? lane : 0), lane < 3 * rows);
+  if (lane < 16) copy_async4(&T.v[32 + lane], w + (lane + 32 < 3 * rows ? lane + 32 : 0), lane + 32 < 3 * rows);
+  copy_commit();
+}
+
+// c[u][m] = sum over the row halves q of z[q][m] b[u][q], for two column pairs u
+// and the two fragments m of 32 outputs
+__device__ __forceinline__ void weight_products(float (&c)[2][2][4], const uint32_t (&zh)[2][2][4],
+                                                const uint32_t (&zl)[2][2][4], const uint32_t (&bh)[2][2][2],
+                                                const uint32_t (&bl)[2][2][2]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          mma_from(q == 0 && p == 0, c[u][m], p == 0 ? zl[q][m] : zh[q][m], p == 1 ? bl[u][q] : bh[u][q]);
 }
 
 struct CellsBackwardArgs {
@@ -418,54 +538,56 @@ __device__ __forceinline__ void backward_w1(const CellsBackwardArgs& P, CellsBac
     S.lo[warp][q * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   __syncwarp();
+  const Base base0(g), base1(8 + g);
   float acc[2][8][4] = {};
+  fetch_tile(S.tile[warp][0], lane, hidden, P.d_raw, P.x, row0, cell_end);
+  int stage = 0;
 #pragma unroll 1
-  for (; tiles > 0; --tiles, row0 += CB_ROWS) {
+  for (; tiles > 0; --tiles, row0 += CB_ROWS, stage ^= 1) {
+    if (tiles > 1) {
+      fetch_tile(S.tile[warp][stage ^ 1], lane, hidden, P.d_raw, P.x, row0 + CB_ROWS, cell_end);
+      copy_wait<1>();
+    } else {
+      copy_wait<0>();
+    }
+    __syncwarp();
+    const BackwardTile& T = S.tile[warp][stage];
     // g2 as operand B: features 8t .. 8t + 7 of rows g and g + 8; then g1 = (W2^T g2) (h1 > 0)
     float dz[2][2][4];                       // [rows 0-7, 8-15][m tile]
     float4 gr[2];
     float mask[2][8];
-    bool on[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int64_t r = row0 + 8 * q + g;
-      on[q] = r < cell_end;
-      const int64_t rc = on[q] ? r : cell_end - 1;
-      gr[q] = __ldg(reinterpret_cast<const float4*>(P.d_raw) + rc);
-      const float4 m0 = __ldg(reinterpret_cast<const float4*>(hidden) + rc * 16 + 8 + 2 * t);
-      const float4 m1 = __ldg(reinterpret_cast<const float4*>(hidden) + rc * 16 + 9 + 2 * t);
+      gr[q] = T.d_raw[8 * q + g];
+      const float4 m0 = *reinterpret_cast<const float4*>(&T.hidden[8 * q + g][32 + 8 * t]);
+      const float4 m1 = *reinterpret_cast<const float4*>(&T.hidden[8 * q + g][36 + 8 * t]);
       mask[q][0] = m0.x, mask[q][1] = m0.y, mask[q][2] = m0.z, mask[q][3] = m0.w;
       mask[q][4] = m1.x, mask[q][5] = m1.y, mask[q][6] = m1.z, mask[q][7] = m1.w;
     }
-    float h1[2][4][2], px[2][2][3];          // of rows 8q + 2t + i: the k of the weight products
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t r = min(row0 + 8 * q + 2 * t + i, cell_end - 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h1[q][j][i] = __ldg(hidden + r * 64 + 8 * j + g);
-#pragma unroll
-        for (int c = 0; c < 3; ++c) px[q][i][c] = __ldg(P.x + r * 3 + c);
-      }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const float4 w0 = S.wh[warp][8 * t + 2 * s], w1 = S.wh[warp][8 * t + 2 * s + 1];
       uint32_t bh[2][2], bl[2][2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        split3(on[q] && mask[q][2 * s] > 0.0f ? head_grad(w0, gr[q]) : 0.0f, bh[q][0], bl[q][0]);
-        split3(on[q] && mask[q][2 * s + 1] > 0.0f ? head_grad(w1, gr[q]) : 0.0f, bh[q][1], bl[q][1]);
+        split3(mask[q][2 * s] > 0.0f ? head_grad(w0, gr[q]) : 0.0f, bh[q][0], bl[q][0]);
+        split3(mask[q][2 * s + 1] > 0.0f ? head_grad(w1, gr[q]) : 0.0f, bh[q][1], bl[q][1]);
       }
+      uint32_t wh[2][4], wl[2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint4 hi = S.hi[warp][(m * 4 + s) * 32 + lane], lo = S.lo[warp][(m * 4 + s) * 32 + lane];
-        const uint32_t ahi[4] = {hi.x, hi.y, hi.z, hi.w}, alo[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (s == 0) mma3_first(dz[q][m], ahi, alo, bh[q], bl[q]);
-          else mma3(dz[q][m], ahi, alo, bh[q], bl[q]);
+        wh[m][0] = hi.x, wh[m][1] = hi.y, wh[m][2] = hi.z, wh[m][3] = hi.w;
+        wl[m][0] = lo.x, wl[m][1] = lo.y, wl[m][2] = lo.z, wl[m][3] = lo.w;
       }
+      // the three products of an accumulator stand four instructions apart, here and below
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            mma_from(s == 0 && p == 0, dz[q][m], p == 0 ? wl[m] : wh[m], p == 1 ? bl[q] : bh[q]);
     }
     // C's (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1) are A's (g, t), (g, t+4), (g+8, t), (g+8, t+4)
     uint32_t zh[2][2][4], zl[2][2][4];
@@ -475,7 +597,7 @@ __device__ __forceinline__ void backward_w1(const CellsBackwardArgs& P, CellsBac
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          split3(h1[q][2 * m + (i >> 1)][i & 1] > 0.0f ? dz[q][m][i] : 0.0f,
+          split3(T.hidden[8 * q + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] > 0.0f ? dz[q][m][i] : 0.0f,
                  zh[q][m][(i & 1) * 2 + (i >> 1)], zl[q][m][(i & 1) * 2 + (i >> 1)]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -483,25 +605,28 @@ __device__ __forceinline__ void backward_w1(const CellsBackwardArgs& P, CellsBac
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) position_base(px[q][i], 8 * j + g, 1.0f, e[q][i]);
+        for (int i = 0; i < 2; ++i) (j ? base1 : base0).encode(&T.v[3 * (8 * q + 2 * t + i)], 1.0f, e[q][i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t bh[2][2], bl[2][2];
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t bh[2][2][2], bl[2][2][2];     // [column pair][row half]
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          split3(e[q][0][i], bh[q][0], bl[q][0]);
-          split3(e[q][1][i], bh[q][1], bl[q][1]);
-        }
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float c[4];
-          mma3_first(c, zh[0][m], zl[0][m], bh[0], bl[0]);
-          mma3(c, zh[1][m], zl[1][m], bh[1], bl[1]);
+          for (int q = 0; q < 2; ++q) {
+            split3(e[q][0][i + u], bh[u][q][0], bl[u][q][0]);
+            split3(e[q][1][i + u], bh[u][q][1], bl[u][q][1]);
+          }
+        float c[2][2][4];
+        weight_products(c, zh, zl, bh, bl);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][4 * j + i][k] += c[k];
-        }
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[m][4 * j + i + u][k] += c[u][m][k];
       }
     }
+    __syncwarp();                            // this stage may be overwritten
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -522,27 +647,31 @@ __device__ __forceinline__ void backward_w2(const CellsBackwardArgs& P, CellsBac
   const int g = lane >> 2, t = lane & 3;
   const float* __restrict__ hidden = P.hidden;
   float acc[2][4][4] = {}, ah[4][4] = {}, sb2[4] = {};
+  fetch_tile(S.tile[warp][0], lane, hidden, P.d_raw, P.d, row0, cell_end);
+  int stage = 0;
 #pragma unroll 1
-  for (; tiles > 0; --tiles, row0 += CB_ROWS) {
-    float h1[2][4][2], h2[2][4][2], gc[2][2], dd[2][2][3];
+  for (; tiles > 0; --tiles, row0 += CB_ROWS, stage ^= 1) {
+    if (tiles > 1) {
+      fetch_tile(S.tile[warp][stage ^ 1], lane, hidden, P.d_raw, P.d, row0 + CB_ROWS, cell_end);
+      copy_wait<1>();
+    } else {
+      copy_wait<0>();
+    }
+    __syncwarp();
+    BackwardTile& T = S.tile[warp][stage];
+    if (lane < CB_ROWS && row0 + lane < cell_end) unit3(&T.v[3 * lane]);
+    __syncwarp();
+    float h2[2][4][2], gc[2][2];
     float4 gr[2][2];
-    bool on[2][2];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t r0 = row0 + 8 * q + 2 * t + i;
-        on[q][i] = r0 < cell_end;
-        const int64_t r = on[q][i] ? r0 : cell_end - 1;
-        gr[q][i] = __ldg(reinterpret_cast<const float4*>(P.d_raw) + r);
-        gc[q][i] = on[q][i] && g < 4 ? __ldg(P.d_raw + r * 4 + (g & 3)) : 0.0f;
+        const int r = 8 * q + 2 * t + i;
+        gr[q][i] = T.d_raw[r];
+        gc[q][i] = g < 4 ? reinterpret_cast<const float*>(&T.d_raw[r])[g & 3] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h1[q][j][i] = __ldg(hidden + r * 64 + 8 * j + g);
-          h2[q][j][i] = __ldg(hidden + r * 64 + 32 + 8 * j + g);
-        }
-#pragma unroll
-        for (int c = 0; c < 3; ++c) dd[q][i][c] = __ldg(P.d + r * 3 + c);
+        for (int j = 0; j < 4; ++j) h2[q][j][i] = T.hidden[r][32 + 8 * j + g];
       }
     // g2 as operand A: features g + 8 j of rows 8q + 2t + i
     uint32_t zh[2][2][4], zl[2][2][4];
@@ -553,27 +682,29 @@ __device__ __forceinline__ void backward_w2(const CellsBackwardArgs& P, CellsBac
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float z = on[q][i] && h2[q][j][i] > 0.0f ? head_grad(w, gr[q][i]) : 0.0f;
+          const float z = h2[q][j][i] > 0.0f ? head_grad(w, gr[q][i]) : 0.0f;
           sb2[j] += z;
           split3(z, zh[q][j >> 1][(j & 1) + 2 * i], zl[q][j >> 1][(j & 1) + 2 * i]);
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t bh[2][2], bl[2][2];
+    for (int j = 0; j < 4; j += 2) {
+      uint32_t bh[2][2][2], bl[2][2][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        split3(h1[q][j][0], bh[q][0], bl[q][0]);
-        split3(h1[q][j][1], bh[q][1], bl[q][1]);
-      }
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        float c[4];
-        mma3_first(c, zh[0][m], zl[0][m], bh[0], bl[0]);
-        mma3(c, zh[1][m], zl[1][m], bh[1], bl[1]);
+        for (int q = 0; q < 2; ++q) {
+          split3(T.hidden[8 * q + 2 * t][8 * (j + u) + g], bh[u][q][0], bl[u][q][0]);
+          split3(T.hidden[8 * q + 2 * t + 1][8 * (j + u) + g], bh[u][q][1], bl[u][q][1]);
+        }
+      float c[2][2][4];
+      weight_products(c, zh, zl, bh, bl);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[m][j][k] += c[k];
-      }
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][j + u][k] += c[u][m][k];
     }
     // the heads: rows of A are features of [h2 | gamma(d)], columns of B the channels
     uint32_t gh[2][2], gl[2][2];
@@ -589,33 +720,36 @@ __device__ __forceinline__ void backward_w2(const CellsBackwardArgs& P, CellsBac
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float* e = dd[q][i];
-        const float u = (g < 2 || g == 6 ? e[0] : g < 4 || g == 7 ? e[1] : e[2]) / norm3(e);
-        const float u2 = __shfl_sync(0xffffffffu, u, 16 + t);
-        two_octaves(u, 2 * (g & 1), v[q][i]);
+        const float* e = &T.v[3 * (8 * q + 2 * t + i)];
+        two_octaves(e[g < 6 ? g >> 1 : g - 6], g & 1 ? 4.0f : 1.0f, v[q][i]);
         if (g >= 6) {
-          v[q][i][0] = u;
-          v[q][i][2] = g == 6 ? u2 : 1.0f;
+          v[q][i][0] = e[g - 6];
+          v[q][i][2] = g == 6 ? e[2] : 1.0f;
           v[q][i][1] = v[q][i][3] = 0.0f;
         }
       }
+    float c[4][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      float c[4];
+    for (int q = 0; q < 2; ++q) {
+      uint32_t fh[4][4], fl[4][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t fh[4], fl[4];
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            split3(m < 2 ? h2[q][2 * m + k][i] : v[q][i][2 * (m - 2) + k], fh[2 * i + k], fl[2 * i + k]);
-        if (q == 0) mma3_first(c, fh, fl, gh[q], gl[q]);
-        else mma3(c, fh, fl, gh[q], gl[q]);
-      }
+            split3(m < 2 ? h2[q][2 * m + k][i] : v[q][i][2 * (m - 2) + k], fh[m][2 * i + k], fl[m][2 * i + k]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ah[m][k] += c[k];
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          mma_from(q == 0 && p == 0, c[m], p == 0 ? fl[m] : fh[m], p == 1 ? gl[q] : gh[q]);
     }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ah[m][k] += c[m][k];
+    __syncwarp();                            // this stage may be overwritten
   }
   G -= O_W2;                                 // by the blob's offsets below
 #pragma unroll
@@ -730,7 +864,8 @@ cudaError_t launch_cells_forward(const float* x, const float* d, int64_t n, cons
   cudaError_t e = cudaFuncSetAttribute(cells_forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (n + CF_ROWS - 1) / CF_ROWS + (n_cells < n ? n_cells : n);
-  const unsigned grid = (unsigned)(tiles < 148 * CF_PER_SM ? tiles : 148 * CF_PER_SM);
+  constexpr int64_t most = 148 * CF_PER_SM * CF_WAVES;
+  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
   cells_forward_kernel<<<grid, CF_THREADS, sm, st>>>(x, d, n, offset, n_cells, cell_w, raw, hidden);
   return cudaGetLastError();
 }

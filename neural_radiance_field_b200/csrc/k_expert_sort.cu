@@ -121,8 +121,10 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
   }
 }
 
+// BITS: bits of an id, rounded up to a value that is instantiated.
+template <int BITS>
 __global__ void __launch_bounds__(ES_T)
-sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts, int bits,
+sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   const int32_t* __restrict__ table, const int32_t* __restrict__ totals,
                   int32_t* __restrict__ offset, int32_t* __restrict__ order, int32_t* __restrict__ pos) {
   // base[e]: the next sorted row of expert e for this CTA; words of two 16-bit
@@ -195,39 +197,39 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
         }
     }
     __syncthreads();
+    const uint32_t lower = (1u << lane) - 1u;
     for (int64_t i0 = r0; i0 < r1; i0 += 128) {
+      const int32_t* src = ids + i0 + lane;
+      const int left = (int)min((int64_t)128, r1 - i0) - lane;   // this lane's pairs: 32 q < left
       int id[4];
       uint32_t peers[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t i = i0 + 32 * q + lane;
-        id[q] = i < r1 ? __ldg(ids + i) : -1;
+        id[q] = 32 * q < left ? __ldg(src + 32 * q) : -1;
         if ((unsigned)id[q] >= (unsigned)n_experts) id[q] = -1;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
         peers[q] = __ballot_sync(0xffffffffu, id[q] >= 0);
-        for (int b = 0; b < bits; ++b) {
-          const uint32_t bal = __ballot_sync(0xffffffffu, (id[q] >> b) & 1);
-          peers[q] &= (id[q] >> b) & 1 ? bal : ~bal;
-        }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t i = i0 + 32 * q + lane;
-        int32_t p = -1;
-        if (id[q] >= 0) {
-          const int shift = 16 * (id[q] & 1), below = __popc(peers[q] & ((1u << lane) - 1u));
-          p = base[id[q]] + (int32_t)((mine[id[q] >> 1] >> shift) & 0xffffu) + below;
+      for (int b = 0; b < BITS; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool set = id[q] & (1 << b);
+          const uint32_t bal = __ballot_sync(0xffffffffu, set);
+          peers[q] &= set ? bal : ~bal;
         }
+      int32_t* dst = pos + i0 + lane;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        int32_t p = -1;
+        const int at = id[q] >> 1, shift = 16 * (id[q] & 1);
+        if (id[q] >= 0) p = base[id[q]] + (int32_t)((mine[at] >> shift) & 0xffffu) + __popc(peers[q] & lower);
         __syncwarp();
         if (id[q] >= 0) {
           // one lane a peer group; the word's other expert may have one too, so the add is atomic
-          if ((peers[q] & ((1u << lane) - 1u)) == 0)
-            atomicAdd(&mine[id[q] >> 1], (uint32_t)__popc(peers[q]) << (16 * (id[q] & 1)));
-          if (order) order[p] = (int32_t)i;
+          if ((peers[q] & lower) == 0) atomicAdd(&mine[at], (uint32_t)__popc(peers[q]) << shift);
+          if (order) order[p] = (int32_t)i0 + lane + 32 * q;
         }
-        if (i < r1) pos[i] = p;
+        if (32 * q < left) dst[32 * q] = p;
         __syncwarp();
       }
     }
@@ -263,16 +265,18 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts,
   int32_t* table = (int32_t*)work;
   int32_t* totals = table + (int64_t)plan.ctas * n_experts;
   const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
-  cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
-  if (e != cudaSuccess) return e;
-  int bits = 0;
-  while ((1 << bits) < n_experts) ++bits;
   sort_count_kernel<<<plan.ctas, ES_T, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
   sort_columns_kernel<<<(n_experts + 31) / 32, 1024, 0, st>>>(table, plan.ctas, n_experts, totals);
-  sort_place_kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, bits, table, totals,
-                                                       offset, order, pos);
-  return cudaGetLastError();
+  auto place = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
+    if (e != cudaSuccess) return e;
+    kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, table, totals, offset, order, pos);
+    return cudaGetLastError();
+  };
+  if (n_experts <= 16) return place(sort_place_kernel<4>);
+  if (n_experts <= 256) return place(sort_place_kernel<8>);
+  return place(sort_place_kernel<12>);
 }
 
 }  // namespace nerfb
