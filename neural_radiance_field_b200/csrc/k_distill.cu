@@ -9,12 +9,16 @@
 // team: a warp (rows up to 16 KB, where there are rows enough to fill the GPU:
 // no barrier anywhere), a CTA of 256 threads (up to 64 KB), or a cluster of two
 // to eight such CTAs (up to 512 KB), which join their statistics through
-// distributed shared memory. Longer rows are streamed twice, the second time
+// distributed shared memory. A CTA goes from row to row, and as soon as a vector
+// of the gradient is written its register takes the next row's vector, so that
+// row's loads run under this row's stores and barriers. Longer rows are streamed twice, the second time
 // from L2, by clusters of eight. Warp 0 of a CTA works out the teacher's
 // probabilities while the row's loads are in flight. A row's 16-byte vectors
 // start wherever its address allows; up to 14 elements before and after them go
 // one by one.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "nerf_experts.cuh"
 #include "nerf_vec.cuh"
@@ -79,57 +83,86 @@ __device__ __forceinline__ float2 cta_join(float2 v, float c, float2* red) {
   return warp_join((threadIdx.x & 31) < W ? red[threadIdx.x & 31] : make_float2(-INFINITY, 0.0f), c);
 }
 
+__device__ __forceinline__ float warp_sum(float v) { return warp_fold(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ float warp_max(float v) { return warp_fold(v, [](float a, float b) { return max_nan(a, b); }); }
+
 // The teacher's side of a row, by one warp: probabilities of its kept entries
-// (0 for the others) and sum_j p_j log p_j, the same in every lane. `some`: an
-// entry is kept.
-__device__ __forceinline__ float teacher_probs(const DistillArgs& A, int64_t i, float* probs, bool& some) {
+// (0 for the others) in `probs` and, of lane l, entry l's id (-1: not kept) and
+// probability; sum_j p_j log p_j, the same in every lane. `some`: an entry is kept.
+struct Teacher {
+  bool some;
+  int32_t id;
+  float p, plogp;
+};
+__device__ __forceinline__ Teacher teacher_row(const DistillArgs& A, int64_t i, float* probs) {
   const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / A.temperature;
   const float* tl = A.tl + i * A.k;
   const int32_t* ti = A.ti + i * A.k;
+  Teacher R{false, -1, 0.0f, 0.0f};
+  float y = -INFINITY;
+  if (lane < A.k) {
+    const int32_t id = __ldg(ti + lane);
+    y = __ldg(tl + lane);
+    if ((unsigned)id < (unsigned)A.classes && y != -INFINITY) R.id = id; else y = -INFINITY;
+  }
+  if (A.k <= 32) {                           // all of it in registers
+    const float top = warp_max(y);
+    R.some = top != -INFINITY;
+    if (!R.some) {
+      if (lane < A.k) probs[lane] = 0.0f;
+      return R;
+    }
+    const float z = (y - top) * inv_t, e = R.id >= 0 ? expf(z) : 0.0f, norm = warp_sum(e);
+    R.p = e / norm;
+    if (lane < A.k) probs[lane] = R.p;
+    R.plogp = warp_sum(R.p != 0.0f ? R.p * (z - logf(norm)) : 0.0f);
+    return R;
+  }
   auto kept = [&](int j) { return (unsigned)__ldg(ti + j) < (unsigned)A.classes && __ldg(tl + j) != -INFINITY; };
-  float top = -INFINITY;
-  for (int j = lane; j < A.k; j += 32)
+  float top = y;
+  for (int j = lane + 32; j < A.k; j += 32)
     if (kept(j)) top = max_nan(top, __ldg(tl + j));
-  top = warp_fold(top, [](float a, float b) { return max_nan(a, b); });
-  some = top != -INFINITY;
+  top = warp_max(top);
+  R.some = top != -INFINITY;
   float norm = 0.0f;
   for (int j = lane; j < A.k; j += 32) {
     const float e = kept(j) ? expf((__ldg(tl + j) - top) * inv_t) : 0.0f;
     probs[j] = e;
     norm += e;
   }
-  norm = warp_fold(norm, [](float a, float b) { return a + b; });
+  norm = warp_sum(norm);
   const float log_norm = logf(norm);
   float l = 0.0f;
   for (int j = lane; j < A.k; j += 32) {
-    const float p = some ? probs[j] / norm : 0.0f;
+    const float p = R.some ? probs[j] / norm : 0.0f;
     probs[j] = p;
     if (p != 0.0f) l += p * ((__ldg(tl + j) - top) * inv_t - log_norm);
   }
-  return warp_fold(l, [](float a, float b) { return a + b; });
+  R.p = lane < A.k ? probs[lane] : 0.0f;
+  R.plogp = warp_sum(l);
+  return R;
 }
 
 // The row's loss, by the warp that has its teacher's side.
 template <typename T>
 __device__ __forceinline__ void write_loss(const DistillArgs& A, int64_t i, const T* s, float m, float z,
-                                           const float* probs, float plogp, bool some) {
+                                           const float* probs, const Teacher& R) {
   const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / A.temperature, log_z = logf(z);
-  const int32_t* ti = A.ti + i * A.k;
-  float l = 0.0f;
-  for (int j = lane; j < A.k; j += 32)
-    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[__ldg(ti + j)]) - m) * inv_t - log_z);
-  l = warp_fold(l, [](float a, float b) { return a + b; });
-  if (lane == 0) A.loss[i] = some ? A.temperature * A.temperature * (plogp - l) : 0.0f;
+  float l = R.p != 0.0f ? R.p * ((elem_to_f<T>(s[R.id]) - m) * inv_t - log_z) : 0.0f;
+  for (int j = lane + 32; j < A.k; j += 32)
+    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[__ldg(A.ti + i * A.k + j)]) - m) * inv_t - log_z);
+  l = warp_sum(l);
+  if (lane == 0) A.loss[i] = R.some ? A.temperature * A.temperature * (R.plogp - l) : 0.0f;
 }
 
 // The gradient of the kept classes in [lo, hi), which the row's pass wrote as q
 // alone: less the teacher's probability, summed where an id comes twice (its
-// first entry writes). `r` of `team` threads.
+// first entry writes). `r` of `team` threads. aiz: row scale * T / Z.
 template <typename T>
 __device__ __forceinline__ void kept_gradients(const DistillArgs& A, int r, int team, int64_t i, const T* s,
-                                               T* g, float m, float c, float a, float iz, const float* probs,
+                                               T* g, float m, float c, float a, float aiz, const float* probs,
                                                int lo, int hi) {
   const int32_t* ti = A.ti + i * A.k;
   for (int j = r; j < A.k; j += team) {
@@ -142,11 +175,27 @@ __device__ __forceinline__ void kept_gradients(const DistillArgs& A, int r, int 
         first = first && q >= j;
         p += probs[q];
       }
-    if (first) g[id] = elem_from_f<T>(a * (exp2_fast((elem_to_f<T>(s[id]) - m) * c) * iz - p));
+    if (first) g[id] = elem_from_f<T>(fmaf(exp2_fast((elem_to_f<T>(s[id]) - m) * c), aiz, -a * p));
   }
+}
+// The same by one warp that has the teacher's entries in registers (k <= 32):
+// equal ids find each other by a match.
+template <typename T>
+__device__ __forceinline__ void kept_gradients_warp(const DistillArgs& A, const Teacher& R, const T* s, T* g,
+                                                    float m, float c, float a, float aiz, const float* probs) {
+  const int lane = threadIdx.x & 31;
+  const unsigned peers = __match_any_sync(0xffffffffu, R.id);
+  if (R.id < 0 || lane != __ffs(peers) - 1) return;
+  float p = 0.0f;
+  for (unsigned left = peers; left; left &= left - 1) p += probs[__ffs(left) - 1];
+  g[R.id] = elem_from_f<T>(fmaf(exp2_fast((elem_to_f<T>(s[R.id]) - m) * c), aiz, -a * p));
 }
 
 constexpr float kLog2e = 1.44269504f;
+// -inf, once or twice in a word
+template <typename T> constexpr uint32_t kNegInf = 0xff800000u;
+template <> constexpr uint32_t kNegInf<__nv_bfloat16> = 0xff80ff80u;
+template <> constexpr uint32_t kNegInf<__half> = 0xfc00fc00u;
 
 // The part of a row that CTA `rank` of `C` holds: vectors [v0, v1) of the row,
 // and single elements (the first CTA those before the vectors, the last those after).
@@ -171,11 +220,15 @@ struct RowPart {
 
 // Rows in registers: NV vectors a thread and one single element. TEAM 32: a warp
 // a row, eight rows to a CTA; TEAM 256: a CTA, or a cluster of them, a row.
+constexpr int rows_per_sm(int team, int nv) {
+  return nv <= 2 ? 4 : nv <= 8 ? 3 : team == 32 && nv == 32 ? 1 : 2;
+}
 template <typename T, int TEAM, int NV>
-__global__ void __launch_bounds__(256, NV <= 8 ? 3 : TEAM == 32 && NV == 32 ? 1 : 2)
+__global__ void __launch_bounds__(256, rows_per_sm(TEAM, NV))
 distill_rows_kernel(DistillArgs A, int C) {
   using V = Vec<T, 16>;
   constexpr int TEAMS = 256 / TEAM;
+  constexpr bool AHEAD = TEAM != 32;         // load the next row early; other warps hide a warp's loads
   __shared__ float2 red[2][8], stat[2];
   __shared__ float probs_s[TEAMS * DISTILL_MAX_K];
   __shared__ int some_s[2];
@@ -184,41 +237,74 @@ distill_rows_kernel(DistillArgs A, int C) {
   float* probs = probs_s + (TEAM == 32 ? warp * DISTILL_MAX_K : 0);
   const float c = kLog2e / A.temperature;
   const int64_t step = (int64_t)gridDim.x / C * TEAMS;
-  int turn = 0;
-  for (int64_t i = (int64_t)blockIdx.x / C * TEAMS + (TEAM == 32 ? warp : 0); i < A.n; i += step, turn ^= 1) {
+  int64_t i = (int64_t)blockIdx.x / C * TEAMS + (TEAM == 32 ? warp : 0);
+  V v[NV];
+  RowPart P;
+  const uint4* sv;
+  int nv;                                    // this thread's vectors: q * TEAM < nv
+  float one;
+  // row i's part and its vectors' place; the loads are issued by the caller
+  auto enter = [&](int64_t row) {
+    const bool in = row < A.n;
+    const T* s = (const T*)A.student + (in ? row : 0) * A.classes;
+    P = RowPart::of<T, V::N>(s, A.classes, rank, C, r);
+    P.has = P.has && in;
+    sv = reinterpret_cast<const uint4*>(s + P.head) + P.v0 + r;
+    nv = in ? P.v1 - P.v0 - r : 0;
+    one = P.has ? elem_to_f<T>(s[P.single]) : -INFINITY;
+  };
+  // a vector past the part holds -inf: it adds nothing to the statistics, which
+  // are then free of conditions
+  auto take = [&](int q) {
+    v[q].fill(kNegInf<T>);
+    if (q * TEAM < nv) v[q].load(sv, q * TEAM);
+  };
+  if (AHEAD) {
+    enter(i);
+#pragma unroll
+    for (int q = 0; q < NV; ++q) take(q);
+  }
+  for (int turn = 0; i < A.n; i += step, turn ^= 1) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
-    const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, r);
-    const uint4* sv = reinterpret_cast<const uint4*>(s + P.head) + P.v0 + r;
-    const int nv = P.v1 - P.v0 - r;          // this thread's vectors: q * TEAM < nv
-    V v[NV];
+    if (!AHEAD) {
+      enter(i);
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if (q * TEAM < nv) v[q].load(sv + q * TEAM);
-    float one = -INFINITY;
-    if (P.has) one = elem_to_f<T>(s[P.single]);
-    bool some = false;
-    float plogp = 0.0f;
-    if (TEAM == 32 || warp == 0) {
-      plogp = teacher_probs(A, i, probs, some);
-      if (TEAM != 32 && r == 0) some_s[turn] = some;
+      for (int q = 0; q < NV; ++q) take(q);
     }
-    float m = one;
+    Teacher R{false, -1, 0.0f, 0.0f};
+    if (TEAM == 32 || warp == 0) {
+      R = teacher_row(A, i, probs);
+      if (TEAM != 32 && r == 0) some_s[turn] = R.some;
+    }
+    // four maxima and four sums side by side: one chain would wait for itself
+    float mp[4] = {one, one, one, one};
+    // The passes go over groups of four vectors, each behind a condition that the
+    // whole team shares: unused groups are skipped, and a row of 16-bit elements is
+    // never unpacked as a whole, which would not fit the registers.
+    const int used = (P.v1 - P.v0 + TEAM - 1) / TEAM;
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if (q * TEAM < nv)
+    for (int q0 = 0; q0 < NV; q0 += 4)
+      if (q0 < used)
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) m = max_nan(m, v[q].get(e));
-    if (TEAM == 32) m = warp_fold(m, [](float a, float b) { return max_nan(a, b); });
+        for (int q = q0; q < q0 + 4 && q < NV; ++q)
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], v[q].get(e));
+    float m = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
+    if (TEAM == 32) m = warp_max(m);
     const float shift = TEAM != 32 && m == -INFINITY ? 0.0f : m;
-    float z = P.has ? exp2_fast((one - shift) * c) : 0.0f;
+    float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if (q * TEAM < nv)
+    for (int q0 = 0; q0 < NV; q0 += 4)
+      if (q0 < used)
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) z += exp2_fast((v[q].get(e) - shift) * c);
+        for (int q = q0; q < q0 + 4 && q < NV; ++q)
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((v[q].get(e) - shift) * c);
+    float z = (zp[0] + zp[1]) + (zp[2] + zp[3]);
+    bool some = R.some;
     if (TEAM == 32) {
-      z = warp_fold(z, [](float a, float b) { return a + b; });
+      z = warp_sum(z);
       __syncwarp();
     } else {
       float2 all = cta_join<256>(make_float2(m, z), c, red[turn]);
@@ -233,30 +319,42 @@ distill_rows_kernel(DistillArgs A, int C) {
       z = all.y;
       some = some_s[turn];
     }
-    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, plogp, some);
-    if (g) {
-      const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), iz = 1.0f / z;
-      uint4* gv = reinterpret_cast<uint4*>(g + P.head) + P.v0 + r;
-      if (some) {
+    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, R);
+    const RowPart now = P;
+    const int nv_now = nv;
+    const float one_now = one;
+    const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
+    uint4* gv = reinterpret_cast<uint4*>(g + now.head) + now.v0 + r;
+    if (AHEAD) enter(i + step);
 #pragma unroll
-        for (int q = 0; q < NV; ++q)
-          if (q * TEAM < nv) {
-            float f[V::N];
+    for (int q0 = 0; q0 < NV; q0 += 4) {
+      if (g && some && q0 < used) {
 #pragma unroll
-            for (int e = 0; e < V::N; ++e) f[e] = a * (exp2_fast((v[q].get(e) - m) * c) * iz);
-            V o;
-            o.pack(f);
-            gv[q * TEAM] = o.raw;
-          }
-        if (P.has) g[P.single] = elem_from_f<T>(a * (exp2_fast((one - m) * c) * iz));
-      } else {
+        for (int q = q0; q < q0 + 4 && q < NV; ++q) {
+          float f[V::N];
 #pragma unroll
-        for (int q = 0; q < NV; ++q)
-          if (q * TEAM < nv) gv[q * TEAM] = make_uint4(0, 0, 0, 0);
-        if (P.has) g[P.single] = elem_from_f<T>(0.0f);
+          for (int e = 0; e < V::N; ++e) f[e] = exp2_fast((v[q].get(e) - m) * c) * aiz;
+          V o;
+          o.pack(f);
+          if (q * TEAM < nv_now) o.store(gv, q * TEAM);
+        }
+      } else if (g && q0 < used) {
+#pragma unroll
+        for (int q = q0; q < q0 + 4 && q < NV; ++q)
+          if (q * TEAM < nv_now) gv[q * TEAM] = make_uint4(0, 0, 0, 0);
       }
+      if (AHEAD) {
+#pragma unroll
+        for (int q = q0; q < q0 + 4 && q < NV; ++q) take(q);
+      }
+    }
+    if (g) {
+      if (now.has) g[now.single] = elem_from_f<T>(some ? exp2_fast((one_now - m) * c) * aiz : 0.0f);
       if (TEAM == 32) __syncwarp(); else __syncthreads();
-      if (some) kept_gradients<T>(A, r, TEAM, i, s, g, m, c, a, iz, probs, P.lo, P.hi);
+      if (some) {
+        if (TEAM == 32 && A.k <= 32) kept_gradients_warp<T>(A, R, s, g, m, c, a, aiz, probs);
+        else kept_gradients<T>(A, r, TEAM, i, s, g, m, c, a, aiz, probs, now.lo, now.hi);
+      }
     }
     // the next row's probabilities overwrite these
     if (TEAM == 32) __syncwarp(); else __syncthreads();
@@ -271,7 +369,6 @@ template <typename T, int BYTES>
 __global__ void __launch_bounds__(DW_T, 2)
 distill_wide_kernel(DistillArgs A, int C) {
   using V = Vec<T, BYTES>;
-  using Raw = typename V::Raw;
   __shared__ float2 red[2][DW_T / 32], stat[2];
   __shared__ float probs[DISTILL_MAX_K];
   __shared__ int some_s[2];
@@ -283,12 +380,11 @@ distill_wide_kernel(DistillArgs A, int C) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
     const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
-    const Raw* sv = reinterpret_cast<const Raw*>(s + P.head);
-    bool some = false;
-    float plogp = 0.0f;
+    const T* sv = s + P.head;
+    Teacher R{false, -1, 0.0f, 0.0f};
     if (warp == 0) {
-      plogp = teacher_probs(A, i, probs, some);
-      if (t == 0) some_s[turn] = some;
+      R = teacher_row(A, i, probs);
+      if (t == 0) some_s[turn] = R.some;
     }
     // running maximum and sum: the sum is rescaled once per four vectors
     float m = P.has ? elem_to_f<T>(s[P.single]) : -INFINITY, z = P.has && m != -INFINITY ? 1.0f : 0.0f;
@@ -297,7 +393,7 @@ distill_wide_kernel(DistillArgs A, int C) {
       float top = m;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (q0 + u * DW_T < P.v1) v[u].load(sv + q0 + u * DW_T);
+        if (q0 + u * DW_T < P.v1) v[u].load(sv, q0 + u * DW_T);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (q0 + u * DW_T < P.v1)
@@ -321,41 +417,43 @@ distill_wide_kernel(DistillArgs A, int C) {
     }
     m = all.x;
     z = all.y;
-    some = some_s[turn];
-    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, plogp, some);
+    const bool some = some_s[turn];
+    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, R);
     if (g) {
-      const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), iz = 1.0f / z;
-      Raw* gv = reinterpret_cast<Raw*>(g + P.head);
+      const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
+      T* gv = g + P.head;
       for (int q0 = P.v0 + t; q0 < P.v1; q0 += 4 * DW_T) {
         V v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (q0 + u * DW_T < P.v1) v[u].load(sv + q0 + u * DW_T);
+          if (q0 + u * DW_T < P.v1) v[u].load(sv, q0 + u * DW_T);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (q0 + u * DW_T < P.v1) {
             float f[V::N];
 #pragma unroll
             for (int e = 0; e < V::N; ++e)
-              f[e] = some ? a * (exp2_fast((v[u].get(e) - m) * c) * iz) : 0.0f;
+              f[e] = some ? exp2_fast((v[u].get(e) - m) * c) * aiz : 0.0f;
             V o;
             o.pack(f);
-            gv[q0 + u * DW_T] = o.raw;
+            o.store(gv, q0 + u * DW_T);
           }
       }
-      if (P.has) g[P.single] = elem_from_f<T>(some ? a * (exp2_fast((elem_to_f<T>(s[P.single]) - m) * c) * iz) : 0.0f);
+      if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((elem_to_f<T>(s[P.single]) - m) * c) * aiz : 0.0f);
       __syncthreads();
-      if (some) kept_gradients<T>(A, t, DW_T, i, s, g, m, c, a, iz, probs, P.lo, P.hi);
+      if (some) kept_gradients<T>(A, t, DW_T, i, s, g, m, c, a, aiz, probs, P.lo, P.hi);
     }
     __syncthreads();
   }
   if (C > 1) cluster.sync();
 }
 
+// `teams` of C CTAs, but no more than run at the same time: the CTAs of a cluster
+// share a GPC, whose SMs a size of eight does not divide, so fewer clusters fit
+// than SMs x CTAs / C, and a last few started late would run alone.
 template <typename K>
 cudaError_t run_clusters(K kernel, const DistillArgs& A, int64_t teams, int threads, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(teams * C));
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -364,13 +462,27 @@ cudaError_t run_clusters(K kernel, const DistillArgs& A, int64_t teams, int thre
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
+  if (C > 1 && teams > 1) {
+    static std::atomic<int> fit[4] = {};     // of this kernel, by log2 C; the same on every device (sm_100a)
+    std::atomic<int>& f = fit[C == 2 ? 1 : C == 4 ? 2 : 3];
+    int most = f.load(std::memory_order_relaxed);
+    if (most == 0) {
+      cfg.gridDim = dim3((unsigned)C);
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (most < 1) most = 1;
+      f.store(most, std::memory_order_relaxed);
+    }
+    if (teams > most) teams = most;
+  }
+  cfg.gridDim = dim3((unsigned)(teams * C));
   return cudaLaunchKernelEx(&cfg, kernel, A, C);
 }
 
 template <typename T, int TEAM, int NV>
 cudaError_t run_rows(const DistillArgs& A, int C, cudaStream_t st) {
   constexpr int TEAMS = 256 / TEAM;
-  const int64_t want = (A.n + TEAMS - 1) / TEAMS, most = 148 * 16 / C;
+  const int64_t want = (A.n + TEAMS - 1) / TEAMS, most = 148 * rows_per_sm(TEAM, NV) / C;
   return run_clusters(distill_rows_kernel<T, TEAM, NV>, A, want < most ? want : most, 256, C, st);
 }
 
@@ -397,11 +509,12 @@ cudaError_t run_t(const DistillArgs& A, cudaStream_t st) {
   if (A.n >= 1184 && bytes <= 8192) return run_rows<T, 32, 16>(A, 1, st);
   if (A.n >= 1184 && bytes <= 16384) return run_rows<T, 32, 32>(A, 1, st);
   if (bytes <= 16384) return run_rows<T, 256, 4>(A, 1, st);
-  if (bytes <= 32768) return run_rows<T, 256, 8>(A, 1, st);
-  int C = 1;
-  while (bytes / C > 65536) C *= 2;
-  if (C <= 8) return run_rows<T, 256, 16>(A, C, st);
-  return run_wide<T, 16>(A, st);
+  int C = 1;                                 // CTAs of a row: parts of 64 KB at most
+  while (bytes > 65536 * (int64_t)C) C *= 2;
+  if (C > 8) return run_wide<T, 16>(A, st);
+  const int64_t part = (bytes + C - 1) / C + 16;
+  if (part <= 32768) return run_rows<T, 256, 8>(A, C, st);
+  return run_rows<T, 256, 16>(A, C, st);
 }
 
 }  // namespace

@@ -78,12 +78,10 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
                     const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
                     T* __restrict__ rows, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
-  using Raw = typename V::Raw;
   constexpr int U = 4;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
   const bool on = i < n;
-  const Raw* xr = reinterpret_cast<const Raw*>(x) + i * nv;
   for (int j0 = 0; j0 < k; j0 += KC) {
     Pairs<KC> q;
     q.load(pos, weights, i, k, j0, m, on);
@@ -93,7 +91,7 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
         V a[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (v0 + u * G < nv) a[u].load(xr + v0 + u * G);
+          if (v0 + u * G < nv) a[u].load(x, i * nv + v0 + u * G);
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
           if (q.p[j] < 0) continue;
@@ -102,7 +100,7 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
           if (DW) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-              if (v0 + u * G < nv) b[u].load(reinterpret_cast<const Raw*>(other) + row + u * G);
+              if (v0 + u * G < nv) b[u].load(other, row + u * G);
           }
           if (rows) {
 #pragma unroll
@@ -115,7 +113,7 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
                   for (int c = 0; c < V::N; ++c) f[c] = q.w[j] * a[u].get(c);
                   o.pack(f);
                 }
-                reinterpret_cast<Raw*>(rows)[row + u * G] = o.raw;
+                o.store(rows, row + u * G);
               }
           }
           if (DW) {
@@ -137,12 +135,10 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
                    const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
                    T* __restrict__ out, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
-  using Raw = typename V::Raw;
   constexpr int U = KC == 2 ? 4 : 1;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
   const bool on = i < n;
-  const Raw* rr = reinterpret_cast<const Raw*>(rows);
   Pairs<KC> q;
   if (k <= KC) {                             // one pass for the sum and the dot products
     q.load(pos, weights, i, k, 0, m, on);
@@ -155,8 +151,8 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
           if (v0 + u * G < nv) {
 #pragma unroll
             for (int j = 0; j < KC; ++j)
-              if (q.p[j] >= 0) b[u][j].load(rr + (int64_t)q.p[j] * nv + v0 + u * G);
-            if (DW) a[u].load(reinterpret_cast<const Raw*>(x) + i * nv + v0 + u * G);
+              if (q.p[j] >= 0) b[u][j].load(rows, (int64_t)q.p[j] * nv + v0 + u * G);
+            if (DW) a[u].load(x, i * nv + v0 + u * G);
           }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -175,7 +171,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
             if (out) {
               V o;
               o.pack(s);
-              reinterpret_cast<Raw*>(out)[i * nv + v0 + u * G] = o.raw;
+              o.store(out, i * nv + v0 + u * G);
             }
           }
       }
@@ -190,7 +186,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
         V b[KC];
 #pragma unroll
         for (int j = 0; j < KC; ++j)
-          if (q.p[j] >= 0) b[j].load(rr + (int64_t)q.p[j] * nv + v);
+          if (q.p[j] >= 0) b[j].load(rows, (int64_t)q.p[j] * nv + v);
 #pragma unroll
         for (int j = 0; j < KC; ++j)
           if (q.p[j] >= 0) {
@@ -200,7 +196,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
       }
       V o;
       o.pack(s);
-      reinterpret_cast<Raw*>(out)[i * nv + v] = o.raw;
+      o.store(out, i * nv + v);
     }
   if (DW)
     for (int j0 = 0; j0 < k; j0 += KC) {
@@ -209,12 +205,12 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
       if (on)
         for (int v = lane; v < nv; v += G) {
           V a;
-          a.load(reinterpret_cast<const Raw*>(x) + i * nv + v);
+          a.load(x, i * nv + v);
 #pragma unroll
           for (int j = 0; j < KC; ++j) {
             if (q.p[j] < 0) continue;
             V b;
-            b.load(rr + (int64_t)q.p[j] * nv + v);
+            b.load(rows, (int64_t)q.p[j] * nv + v);
 #pragma unroll
             for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a.get(c), b.get(c), dot[j]);
           }

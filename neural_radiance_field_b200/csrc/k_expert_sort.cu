@@ -26,6 +26,8 @@ constexpr int ES_WARPS = 16, ES_T = ES_WARPS * 32;
 constexpr int ES_RUN = 4064;                 // pairs of a warp's run in one tile
 constexpr int ES_TILE = ES_WARPS * ES_RUN;
 static_assert(ES_TILE < 65536 && ES_RUN % 32 == 0, "a tile's counts are 16-bit");
+constexpr int ES_MATCH = 2;                  // of four groups of 32 pairs, those that use a match instruction
+constexpr int ES_MOST_CTAS = 148 * 3;
 constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
 struct SortPlan {
@@ -35,7 +37,7 @@ struct SortPlan {
 // Small tables leave room for three CTAs to an SM; a CTA has 2048 pairs at least,
 // or the tables would outgrow the pairs.
 SortPlan sort_plan(int64_t pairs, int n_experts) {
-  const int64_t most = n_experts <= 1024 ? 148 * 3 : 148, want = (pairs + 2047) / 2048;
+  const int64_t most = n_experts <= 1024 ? ES_MOST_CTAS : 148, want = (pairs + 2047) / 2048;
   const int64_t ctas = want < most ? want : most;
   const int64_t chunk = ((pairs + ctas - 1) / ctas + ES_T - 1) / ES_T * ES_T;
   return {(int)((pairs + chunk - 1) / chunk), chunk};
@@ -78,45 +80,68 @@ sort_small_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts, int
   }
 }
 
-__global__ void __launch_bounds__(ES_T)
+// Calls f(id) for the ids [begin, end), in any order, by `n` threads; 16-byte
+// loads, four in flight a thread, where the ids are aligned for them (begin is a
+// multiple of 32).
+template <typename F>
+__device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, int64_t begin, int64_t end, int t, int n, F f) {
+  int64_t i = begin;
+  if (((uintptr_t)ids & 15) == 0) {
+    const int64_t vecs = (end - begin) / 4;
+    const int4* v = reinterpret_cast<const int4*>(ids + begin);
+    for (int64_t q = t; q < vecs; q += 4 * n) {
+      int4 a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u] = q + u * n < vecs ? __ldg(v + q + u * n) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f(a[u].x), f(a[u].y), f(a[u].z), f(a[u].w);
+    }
+    i += vecs * 4;
+  }
+  for (i += t; i < end; i += n) f(__ldg(ids + i));
+}
+
+constexpr int ES_CT = 1024;
+__global__ void __launch_bounds__(ES_CT)
 sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   int32_t* __restrict__ table) {
   extern __shared__ int32_t hist[];
-  for (int e = threadIdx.x; e < n_experts; e += ES_T) hist[e] = 0;
+  for (int e = threadIdx.x; e < n_experts; e += ES_CT) hist[e] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
-  for (int64_t i = begin + threadIdx.x; i < end; i += 8 * ES_T) {
-    int id[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) id[q] = i + q * ES_T < end ? __ldg(ids + i + q * ES_T) : -1;
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if ((unsigned)id[q] < (unsigned)n_experts) atomicAdd(&hist[id[q]], 1);
-  }
+  for_ids(ids, begin, end, threadIdx.x, ES_CT, [&](int id) {
+    if ((unsigned)id < (unsigned)n_experts) atomicAdd(&hist[id], 1);
+  });
   __syncthreads();
-  for (int e = threadIdx.x; e < n_experts; e += ES_T) table[(int64_t)blockIdx.x * n_experts + e] = hist[e];
+  for (int e = threadIdx.x; e < n_experts; e += ES_CT) table[(int64_t)blockIdx.x * n_experts + e] = hist[e];
 }
 
 // lane = expert, warp = a run of chunks: table becomes the exclusive prefix over
 // the chunks, totals the experts' sums
+constexpr int ES_PER = (ES_MOST_CTAS + 31) / 32;
 __global__ void __launch_bounds__(1024)
 sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int32_t* __restrict__ totals) {
   __shared__ int32_t part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
-  const int per = (chunks + 31) / 32, c0 = min(chunks, warp * per), c1 = min(chunks, c0 + per);
-  int32_t sum = 0;
-  if (e < n_experts)
-    for (int c = c0; c < c1; ++c) sum += table[(int64_t)c * n_experts + e];
+  const int per = (chunks + 31) / 32, c0 = min(chunks, warp * per), n = min(chunks, c0 + per) - c0;
+  int32_t* col = table + (int64_t)c0 * n_experts + e;
+  int32_t v[ES_PER], sum = 0;
+#pragma unroll
+  for (int c = 0; c < ES_PER; ++c) {
+    v[c] = c < n && e < n_experts ? col[(int64_t)c * n_experts] : 0;
+    sum += v[c];
+  }
   part[warp][lane] = sum;
   __syncthreads();
   int32_t run = 0;
-  for (int w = 0; w < warp; ++w) run += part[w][lane];
+#pragma unroll
+  for (int w = 0; w < 31; ++w) run += w < warp ? part[w][lane] : 0;
   if (e < n_experts) {
     if (warp == 31) totals[e] = run + sum;
-    for (int c = c0; c < c1; ++c) {
-      const int32_t v = table[(int64_t)c * n_experts + e];
-      table[(int64_t)c * n_experts + e] = run;
-      run += v;
+#pragma unroll
+    for (int c = 0; c < ES_PER; ++c) {
+      if (c < n) col[(int64_t)c * n_experts] = run;
+      run += v[c];
     }
   }
 }
@@ -138,10 +163,12 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
   uint32_t* mine = counts + warp * words;
   {
     // exclusive scan of the totals, eight experts a thread
-    int32_t v[8], tot = 0;
+    int32_t v[8], before[8], tot = 0;        // before: the chunks before this one
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = 8 * t + j < n_experts ? totals[8 * t + j] : 0;
+      const bool in = 8 * t + j < n_experts;
+      v[j] = in ? totals[8 * t + j] : 0;
+      before[j] = in ? table[(int64_t)blockIdx.x * n_experts + 8 * t + j] : 0;
       tot += v[j];
     }
     int32_t run = tot;
@@ -157,14 +184,12 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (8 * t + j < n_experts) {
-        base[8 * t + j] = run;
+        base[8 * t + j] = run + before[j];
         if (blockIdx.x == 0) offset[8 * t + j] = run;
       }
       run += v[j];
     }
     if (blockIdx.x == 0 && t == ES_T - 1) offset[n_experts] = run;
-    __syncthreads();
-    for (int e = t; e < n_experts; e += ES_T) base[e] += table[(int64_t)blockIdx.x * n_experts + e];
   }
   const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
   for (int64_t tile = begin; tile < end; tile += ES_TILE) {
@@ -173,14 +198,9 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
     const int64_t r0 = tile + (int64_t)warp * run, r1 = min(tile + left, r0 + run);
     for (int q = lane; q < words; q += 32) mine[q] = 0;
     __syncwarp();
-    for (int64_t i = r0 + lane; i < r1; i += 256) {
-      int id[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) id[q] = i + 32 * q < r1 ? __ldg(ids + i + 32 * q) : -1;
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if ((unsigned)id[q] < (unsigned)n_experts) atomicAdd(&mine[id[q] >> 1], 1u << (16 * (id[q] & 1)));
-    }
+    for_ids(ids, r0, max(r0, r1), lane, 32, [&](int id) {
+      if ((unsigned)id < (unsigned)n_experts) atomicAdd(&mine[id >> 1], 1u << (16 * (id & 1)));
+    });
     __syncthreads();
     // counts -> exclusive prefix over the warps, two experts a word
     uint32_t all[ES_WORDS];
@@ -198,21 +218,25 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
     }
     __syncthreads();
     const uint32_t lower = (1u << lane) - 1u;
+    int ahead[2][4];                         // the ids of the next 256 pairs, on their way
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      ahead[q >> 2][q & 3] = r0 + 32 * q + lane < r1 ? __ldg(ids + r0 + 32 * q + lane) : -1;
     for (int64_t i0 = r0; i0 < r1; i0 += 128) {
-      const int32_t* src = ids + i0 + lane;
       const int left = (int)min((int64_t)128, r1 - i0) - lane;   // this lane's pairs: 32 q < left
       int id[4];
       uint32_t peers[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        id[q] = 32 * q < left ? __ldg(src + 32 * q) : -1;
-        if ((unsigned)id[q] >= (unsigned)n_experts) id[q] = -1;
-        peers[q] = __ballot_sync(0xffffffffu, id[q] >= 0);
+        id[q] = (unsigned)ahead[0][q] < (unsigned)n_experts ? ahead[0][q] : -1;
+        ahead[0][q] = ahead[1][q];
+        ahead[1][q] = i0 + 256 + 32 * q + lane < r1 ? __ldg(ids + i0 + 256 + 32 * q + lane) : -1;
+        peers[q] = q < ES_MATCH ? __match_any_sync(0xffffffffu, id[q]) : __ballot_sync(0xffffffffu, id[q] >= 0);
       }
 #pragma unroll
       for (int b = 0; b < BITS; ++b)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = ES_MATCH; q < 4; ++q) {
           const bool set = id[q] & (1 << b);
           const uint32_t bal = __ballot_sync(0xffffffffu, set);
           peers[q] &= set ? bal : ~bal;
@@ -265,7 +289,7 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts,
   int32_t* table = (int32_t*)work;
   int32_t* totals = table + (int64_t)plan.ctas * n_experts;
   const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
-  sort_count_kernel<<<plan.ctas, ES_T, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
+  sort_count_kernel<<<plan.ctas, ES_CT, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
   sort_columns_kernel<<<(n_experts + 31) / 32, 1024, 0, st>>>(table, plan.ctas, n_experts, totals);
   auto place = [&](auto kernel) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

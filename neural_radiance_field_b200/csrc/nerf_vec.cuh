@@ -1,6 +1,8 @@
 // Row elements in fp32, bf16 or fp16 and vectors of them, computed on in fp32.
 #pragma once
 
+#include <string.h>
+
 #include "nerf_internal.cuh"
 
 namespace nerfb {
@@ -14,39 +16,64 @@ template <> __device__ __forceinline__ float elem_from_f(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 elem_from_f(float v) { return __float2bfloat16(v); }
 template <> __device__ __forceinline__ __half elem_from_f(float v) { return __float2half(v); }
 
-// two 16-bit elements as one word
-template <typename T> __device__ __forceinline__ uint32_t pair_from_f(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pair_from_f<__nv_bfloat16>(float lo, float hi) {
+// element i of a word of one fp32 or two 16-bit elements
+template <typename T> __device__ __forceinline__ float word_elem(uint32_t w, int i);
+template <> __device__ __forceinline__ float word_elem<float>(uint32_t w, int) { return __uint_as_float(w); }
+template <> __device__ __forceinline__ float word_elem<__nv_bfloat16>(uint32_t w, int i) {
+  return __uint_as_float(i ? w & 0xffff0000u : w << 16);
+}
+template <> __device__ __forceinline__ float word_elem<__half>(uint32_t w, int i) {
+  return __half2float(__ushort_as_half((unsigned short)(i ? w >> 16 : w & 0xffffu)));
+}
+// the word of one fp32 element (lo) or of two 16-bit ones
+template <typename T> __device__ __forceinline__ uint32_t word_from_f(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t word_from_f<float>(float lo, float) { return __float_as_uint(lo); }
+template <> __device__ __forceinline__ uint32_t word_from_f<__nv_bfloat16>(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
+  uint32_t w;
+  memcpy(&w, &p, 4);
+  return w;
 }
-template <> __device__ __forceinline__ uint32_t pair_from_f<__half>(float lo, float hi) {
+template <> __device__ __forceinline__ uint32_t word_from_f<__half>(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
+  uint32_t w;
+  memcpy(&w, &p, 4);
+  return w;
 }
 
-template <int BYTES> struct VecRaw;
-template <> struct VecRaw<16> { using type = uint4; };
-template <> struct VecRaw<4> { using type = uint32_t; };
-template <> struct VecRaw<2> { using type = uint16_t; };
-
-// N elements of T in one load or store of `BYTES` bytes.
+// N elements of T in one load or store of 16, 4 or 2 bytes, held as 32-bit words
+// (kept as single 16-bit elements they would take a register each).
 template <typename T, int BYTES>
 struct Vec {
-  static constexpr int N = BYTES / (int)sizeof(T);
-  using Raw = typename VecRaw<BYTES>::type;
-  union { Raw raw; T e[N]; uint32_t words[BYTES >= 4 ? BYTES / 4 : 1]; };
-  __device__ __forceinline__ Vec() {}
-  __device__ __forceinline__ void load(const Raw* p) { raw = __ldg(p); }
-  __device__ __forceinline__ float get(int i) const { return elem_to_f<T>(e[i]); }
-  __device__ __forceinline__ void pack(const float* v) {
-    if constexpr (sizeof(T) == 2 && BYTES >= 4) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) words[i] = pair_from_f<T>(v[2 * i], v[2 * i + 1]);
+  static constexpr int N = BYTES / (int)sizeof(T), W = BYTES >= 4 ? BYTES / 4 : 1, PER = 4 / (int)sizeof(T);
+  uint32_t words[W];
+  // vector v of the row or rows that start at p
+  __device__ __forceinline__ void load(const void* p, int64_t v) {
+    if constexpr (BYTES == 16) {
+      const uint4 r = __ldg(reinterpret_cast<const uint4*>(p) + v);
+      words[0] = r.x, words[1 % W] = r.y, words[2 % W] = r.z, words[3 % W] = r.w;
+    } else if constexpr (BYTES == 4) {
+      words[0] = __ldg(reinterpret_cast<const uint32_t*>(p) + v);
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) e[i] = elem_from_f<T>(v[i]);
+      words[0] = __ldg(reinterpret_cast<const uint16_t*>(p) + v);
     }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t v) const {
+    if constexpr (BYTES == 16)
+      reinterpret_cast<uint4*>(p)[v] = make_uint4(words[0], words[1 % W], words[2 % W], words[3 % W]);
+    else if constexpr (BYTES == 4)
+      reinterpret_cast<uint32_t*>(p)[v] = words[0];
+    else
+      reinterpret_cast<uint16_t*>(p)[v] = (uint16_t)words[0];
+  }
+  __device__ __forceinline__ void fill(uint32_t w) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) words[i] = w;
+  }
+  __device__ __forceinline__ float get(int i) const { return word_elem<T>(words[i / PER], i % PER); }
+  __device__ __forceinline__ void pack(const float* v) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) words[i] = word_from_f<T>(v[PER * i], N > 1 ? v[(PER * i + 1) % N] : 0.0f);
   }
 };
 
