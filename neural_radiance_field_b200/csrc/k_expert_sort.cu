@@ -11,11 +11,10 @@
 //            tile of the chunk at a time, every warp counts its own run of the
 //            tile (16-bit counters, two experts a word), the counts are scanned
 //            over the warps, and every warp walks its run in order, 32 pairs at
-//            a time. Which of the 32 share an expert comes from one ballot per
-//            bit of the id (12 at most: a third of what a match instruction
-//            costs), a pair's rank among them is the number of lower lanes, and
-//            the expert's counter advances by their number. Rows come out in
-//            pair order whatever the timing.
+//            a time. A match instruction finds which of the 32 share an expert (a
+//            ballot per bit of the id took longer), a pair's rank among them is
+//            the number of lower lanes, and the expert's counter advances by
+//            their number. Rows come out in pair order whatever the timing.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
@@ -26,7 +25,6 @@ constexpr int ES_WARPS = 16, ES_T = ES_WARPS * 32;
 constexpr int ES_RUN = 4064;                 // pairs of a warp's run in one tile
 constexpr int ES_TILE = ES_WARPS * ES_RUN;
 static_assert(ES_TILE < 65536 && ES_RUN % 32 == 0, "a tile's counts are 16-bit");
-constexpr int ES_MATCH = 2;                  // of four groups of 32 pairs, those that use a match instruction
 constexpr int ES_MOST_CTAS = 148 * 3;
 constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
@@ -80,25 +78,18 @@ sort_small_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts, int
   }
 }
 
-// Calls f(id) for the ids [begin, end), in any order, by `n` threads; 16-byte
-// loads, four in flight a thread, where the ids are aligned for them (begin is a
-// multiple of 32).
+// Calls f(id) for the ids [begin, end) by `n` threads, 16 loads in flight a
+// thread. Neighbouring lanes take neighbouring pairs: pairs further apart are
+// more often of one expert, whose counts a warp's atomics would add one by one.
 template <typename F>
 __device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, int64_t begin, int64_t end, int t, int n, F f) {
-  int64_t i = begin;
-  if (((uintptr_t)ids & 15) == 0) {
-    const int64_t vecs = (end - begin) / 4;
-    const int4* v = reinterpret_cast<const int4*>(ids + begin);
-    for (int64_t q = t; q < vecs; q += 4 * n) {
-      int4 a[4];
+  for (int64_t i = begin + t; i < end; i += 16 * n) {
+    int id[16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) a[u] = q + u * n < vecs ? __ldg(v + q + u * n) : make_int4(-1, -1, -1, -1);
+    for (int u = 0; u < 16; ++u) id[u] = i + u * n < end ? __ldg(ids + i + u * n) : -1;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) f(a[u].x), f(a[u].y), f(a[u].z), f(a[u].w);
-    }
-    i += vecs * 4;
+    for (int u = 0; u < 16; ++u) f(id[u]);
   }
-  for (i += t; i < end; i += n) f(__ldg(ids + i));
 }
 
 constexpr int ES_CT = 1024;
@@ -146,14 +137,13 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
   }
 }
 
-// BITS: bits of an id, rounded up to a value that is instantiated.
-template <int BITS>
 __global__ void __launch_bounds__(ES_T)
 sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   const int32_t* __restrict__ table, const int32_t* __restrict__ totals,
                   int32_t* __restrict__ offset, int32_t* __restrict__ order, int32_t* __restrict__ pos) {
   // base[e]: the next sorted row of expert e for this CTA; words of two 16-bit
-  // counters: [warp][n_experts / 2]
+  // counters, [warp][words]: word w counts experts w (low half) and words + w (two
+  // neighbours in a word would meet in it: a point's experts are often neighbours)
   extern __shared__ int32_t sm[];
   __shared__ int32_t sums[ES_WARPS];
   int32_t* base = sm;
@@ -199,7 +189,8 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
     for (int q = lane; q < words; q += 32) mine[q] = 0;
     __syncwarp();
     for_ids(ids, r0, max(r0, r1), lane, 32, [&](int id) {
-      if ((unsigned)id < (unsigned)n_experts) atomicAdd(&mine[id >> 1], 1u << (16 * (id & 1)));
+      if ((unsigned)id < (unsigned)n_experts)
+        atomicAdd(&mine[id < words ? id : id - words], id < words ? 1u : 1u << 16);
     });
     __syncthreads();
     // counts -> exclusive prefix over the warps, two experts a word
@@ -231,21 +222,13 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
         id[q] = (unsigned)ahead[0][q] < (unsigned)n_experts ? ahead[0][q] : -1;
         ahead[0][q] = ahead[1][q];
         ahead[1][q] = i0 + 256 + 32 * q + lane < r1 ? __ldg(ids + i0 + 256 + 32 * q + lane) : -1;
-        peers[q] = q < ES_MATCH ? __match_any_sync(0xffffffffu, id[q]) : __ballot_sync(0xffffffffu, id[q] >= 0);
+        peers[q] = __match_any_sync(0xffffffffu, id[q]);
       }
-#pragma unroll
-      for (int b = 0; b < BITS; ++b)
-#pragma unroll
-        for (int q = ES_MATCH; q < 4; ++q) {
-          const bool set = id[q] & (1 << b);
-          const uint32_t bal = __ballot_sync(0xffffffffu, set);
-          peers[q] &= set ? bal : ~bal;
-        }
       int32_t* dst = pos + i0 + lane;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         int32_t p = -1;
-        const int at = id[q] >> 1, shift = 16 * (id[q] & 1);
+        const int at = id[q] < words ? id[q] : id[q] - words, shift = id[q] < words ? 0 : 16;
         if (id[q] >= 0) p = base[id[q]] + (int32_t)((mine[at] >> shift) & 0xffffu) + __popc(peers[q] & lower);
         __syncwarp();
         if (id[q] >= 0) {
@@ -262,8 +245,8 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
     for (int u = 0; u < ES_WORDS; ++u) {
       const int q = t + u * ES_T;
       if (q < words) {
-        base[2 * q] += all[u] & 0xffffu;
-        if (2 * q + 1 < n_experts) base[2 * q + 1] += all[u] >> 16;
+        base[q] += all[u] & 0xffffu;
+        if (words + q < n_experts) base[words + q] += all[u] >> 16;
       }
     }
     __syncthreads();
@@ -291,16 +274,12 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts,
   const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
   sort_count_kernel<<<plan.ctas, ES_CT, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
   sort_columns_kernel<<<(n_experts + 31) / 32, 1024, 0, st>>>(table, plan.ctas, n_experts, totals);
-  auto place = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
-    if (e != cudaSuccess) return e;
-    kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, table, totals, offset, order, pos);
-    return cudaGetLastError();
-  };
-  if (n_experts <= 16) return place(sort_place_kernel<4>);
-  if (n_experts <= 256) return place(sort_place_kernel<8>);
-  return place(sort_place_kernel<12>);
+  const cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
+  if (e != cudaSuccess) return e;
+  sort_place_kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, table, totals, offset, order,
+                                                       pos);
+  return cudaGetLastError();
 }
 
 }  // namespace nerfb
