@@ -60,13 +60,8 @@ __device__ __forceinline__ float warp_fold(float v, F f) {
   return v;
 }
 
-// (maximum, sum of 2^(c (v - maximum))) of two sets of logits; sums of an empty
-// set or of -inf alone are 0, and no -inf is taken from -inf
-__device__ __forceinline__ float2 join(float2 a, float2 b, float c) {
-  const float m = max_nan(a.x, b.x);
-  if (m == -INFINITY) return make_float2(m, 0.0f);
-  return make_float2(m, a.y * exp2_fast((a.x - m) * c) + b.y * exp2_fast((b.x - m) * c));
-}
+// (maximum, sum of 2^(c (v - maximum))) of the lanes' sets of logits together; the
+// sum of an empty set or of -inf alone is 0, and no -inf is taken from -inf
 __device__ __forceinline__ float2 warp_join(float2 v, float c) {
   const float m = warp_fold(v.x, [](float a, float b) { return max_nan(a, b); });
   const float z = m == -INFINITY ? 0.0f : v.y * exp2_fast((v.x - m) * c);
@@ -86,109 +81,122 @@ __device__ __forceinline__ float2 cta_join(float2 v, float c, float2* red) {
 __device__ __forceinline__ float warp_sum(float v) { return warp_fold(v, [](float a, float b) { return a + b; }); }
 __device__ __forceinline__ float warp_max(float v) { return warp_fold(v, [](float a, float b) { return max_nan(a, b); }); }
 
-// The teacher's side of a row, by one warp: probabilities of its kept entries
-// (0 for the others) in `probs` and, of lane l, entry l's id (-1: not kept) and
-// probability; sum_j p_j log p_j, the same in every lane. `some`: an entry is kept.
+// What one warp knows of a row's teacher: of lane l, entry l's id (-1: not
+// kept), logit, student logit and, once solved, probability; sum_j p_j log p_j,
+// the same in every lane; whether an entry is kept. Entries past 32 are read
+// from the arrays again where they are needed.
 struct Teacher {
-  bool some;
-  int32_t id;
-  float p, plogp;
+  int32_t id = -1;
+  float y = -INFINITY, s = 0.0f, p = 0.0f, plogp = 0.0f;
+  bool some = false;
 };
-__device__ __forceinline__ Teacher teacher_row(const DistillArgs& A, int64_t i, float* probs) {
+// The loads alone, to be issued well before the rest.
+template <typename T>
+__device__ __forceinline__ Teacher teacher_load(const DistillArgs& A, int64_t i) {
+  const int lane = threadIdx.x & 31;
+  Teacher R;
+  if (i < A.n && lane < A.k) {
+    const int32_t id = __ldg(A.ti + i * A.k + lane);
+    const float y = __ldg(A.tl + i * A.k + lane);
+    if ((unsigned)id < (unsigned)A.classes && y != -INFINITY) {
+      R.id = id;
+      R.y = y;
+      R.s = elem_to_f<T>(((const T*)A.student)[i * A.classes + id]);
+    }
+  }
+  return R;
+}
+// The probabilities, also to probs[k], and the ids to ids[k] (-1: not kept).
+__device__ __forceinline__ void teacher_solve(const DistillArgs& A, int64_t i, Teacher& R, float* probs, int32_t* ids) {
   const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / A.temperature;
   const float* tl = A.tl + i * A.k;
   const int32_t* ti = A.ti + i * A.k;
-  Teacher R{false, -1, 0.0f, 0.0f};
-  float y = -INFINITY;
-  if (lane < A.k) {
-    const int32_t id = __ldg(ti + lane);
-    y = __ldg(tl + lane);
-    if ((unsigned)id < (unsigned)A.classes && y != -INFINITY) R.id = id; else y = -INFINITY;
-  }
-  if (A.k <= 32) {                           // all of it in registers
-    const float top = warp_max(y);
-    R.some = top != -INFINITY;
-    if (!R.some) {
-      if (lane < A.k) probs[lane] = 0.0f;
-      return R;
-    }
-    const float z = (y - top) * inv_t, e = R.id >= 0 ? expf(z) : 0.0f, norm = warp_sum(e);
-    R.p = e / norm;
-    if (lane < A.k) probs[lane] = R.p;
-    R.plogp = warp_sum(R.p != 0.0f ? R.p * (z - logf(norm)) : 0.0f);
-    return R;
-  }
   auto kept = [&](int j) { return (unsigned)__ldg(ti + j) < (unsigned)A.classes && __ldg(tl + j) != -INFINITY; };
-  float top = y;
+  float top = R.y;
   for (int j = lane + 32; j < A.k; j += 32)
     if (kept(j)) top = max_nan(top, __ldg(tl + j));
   top = warp_max(top);
   R.some = top != -INFINITY;
-  float norm = 0.0f;
-  for (int j = lane; j < A.k; j += 32) {
-    const float e = kept(j) ? expf((__ldg(tl + j) - top) * inv_t) : 0.0f;
-    probs[j] = e;
-    norm += e;
-  }
+  const float z = (R.y - top) * inv_t;
+  float norm = R.id >= 0 ? expf(z) : 0.0f;
+  R.p = norm;
+  for (int j = lane + 32; j < A.k; j += 32)
+    if (kept(j)) norm += expf((__ldg(tl + j) - top) * inv_t);
   norm = warp_sum(norm);
   const float log_norm = logf(norm);
-  float l = 0.0f;
-  for (int j = lane; j < A.k; j += 32) {
-    const float p = R.some ? probs[j] / norm : 0.0f;
-    probs[j] = p;
-    if (p != 0.0f) l += p * ((__ldg(tl + j) - top) * inv_t - log_norm);
+  R.p = R.id >= 0 ? R.p / norm : 0.0f;
+  float l = R.p != 0.0f ? R.p * (z - log_norm) : 0.0f;
+  if (lane < A.k) {
+    probs[lane] = R.p;
+    ids[lane] = R.id;
   }
-  R.p = lane < A.k ? probs[lane] : 0.0f;
+  for (int j = lane + 32; j < A.k; j += 32) {
+    const bool in = kept(j);
+    const float w = (__ldg(tl + j) - top) * inv_t, p = in ? expf(w) / norm : 0.0f;
+    probs[j] = p;
+    ids[j] = in ? __ldg(ti + j) : -1;
+    if (p != 0.0f) l += p * (w - log_norm);
+  }
   R.plogp = warp_sum(l);
-  return R;
 }
 
-// The row's loss, by the warp that has its teacher's side.
+// The row's loss, by the warp that has its teacher.
 template <typename T>
 __device__ __forceinline__ void write_loss(const DistillArgs& A, int64_t i, const T* s, float m, float z,
-                                           const float* probs, const Teacher& R) {
+                                           const float* probs, const int32_t* ids, const Teacher& R) {
   const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / A.temperature, log_z = logf(z);
-  float l = R.p != 0.0f ? R.p * ((elem_to_f<T>(s[R.id]) - m) * inv_t - log_z) : 0.0f;
+  float l = R.p != 0.0f ? R.p * ((R.s - m) * inv_t - log_z) : 0.0f;
   for (int j = lane + 32; j < A.k; j += 32)
-    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[__ldg(A.ti + i * A.k + j)]) - m) * inv_t - log_z);
+    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[ids[j]]) - m) * inv_t - log_z);
   l = warp_sum(l);
   if (lane == 0) A.loss[i] = R.some ? A.temperature * A.temperature * (R.plogp - l) : 0.0f;
 }
 
 // The gradient of the kept classes in [lo, hi), which the row's pass wrote as q
 // alone: less the teacher's probability, summed where an id comes twice (its
-// first entry writes). `r` of `team` threads. aiz: row scale * T / Z.
+// first entry writes). Thread `r` of `team`. aiz: row scale * T / Z.
 template <typename T>
-__device__ __forceinline__ void kept_gradients(const DistillArgs& A, int r, int team, int64_t i, const T* s,
-                                               T* g, float m, float c, float a, float aiz, const float* probs,
-                                               int lo, int hi) {
-  const int32_t* ti = A.ti + i * A.k;
-  for (int j = r; j < A.k; j += team) {
-    const int32_t id = __ldg(ti + j);
+__device__ __forceinline__ void kept_gradients(int k, int r, int team, const T* s, T* g, float m, float c, float a,
+                                               float aiz, const float* probs, const int32_t* ids, int lo, int hi) {
+  for (int j = r; j < k; j += team) {
+    const int32_t id = ids[j];
     if (id < lo || id >= hi) continue;
+    const float v = elem_to_f<T>(s[id]);
     float p = 0.0f;
     bool first = true;
-    for (int q = 0; q < A.k; ++q)
-      if (__ldg(ti + q) == id) {
+    for (int q = 0; q < k; ++q)
+      if (ids[q] == id) {
         first = first && q >= j;
         p += probs[q];
       }
-    if (first) g[id] = elem_from_f<T>(fmaf(exp2_fast((elem_to_f<T>(s[id]) - m) * c), aiz, -a * p));
+    if (first) g[id] = elem_from_f<T>(fmaf(exp2_fast((v - m) * c), aiz, -a * p));
   }
 }
 // The same by one warp that has the teacher's entries in registers (k <= 32):
 // equal ids find each other by a match.
 template <typename T>
-__device__ __forceinline__ void kept_gradients_warp(const DistillArgs& A, const Teacher& R, const T* s, T* g,
-                                                    float m, float c, float a, float aiz, const float* probs) {
+__device__ __forceinline__ void kept_gradients_warp(const Teacher& R, T* g, float m, float c, float a, float aiz,
+                                                    const float* probs) {
   const int lane = threadIdx.x & 31;
   const unsigned peers = __match_any_sync(0xffffffffu, R.id);
   if (R.id < 0 || lane != __ffs(peers) - 1) return;
   float p = 0.0f;
   for (unsigned left = peers; left; left &= left - 1) p += probs[__ffs(left) - 1];
-  g[R.id] = elem_from_f<T>(fmaf(exp2_fast((elem_to_f<T>(s[R.id]) - m) * c), aiz, -a * p));
+  g[R.id] = elem_from_f<T>(fmaf(exp2_fast((R.s - m) * c), aiz, -a * p));
+}
+
+// A CTA's (maximum, sum) joined over its cluster: every CTA writes its own to all,
+// and one cluster barrier later each has them all at hand. `stat` is one of two
+// sets used in turn: a set is written again only after the next row's barrier,
+// which no CTA passes before all have read it.
+__device__ __forceinline__ float2 cluster_join(float2 v, float c, float2* stat, int rank, int C) {
+  cg::cluster_group cluster = cg::this_cluster();
+  if ((int)threadIdx.x < C) cluster.map_shared_rank(stat, threadIdx.x)[rank] = v;
+  cluster.sync();
+  const int lane = threadIdx.x & 31;
+  return warp_join(lane < C ? stat[lane] : make_float2(-INFINITY, 0.0f), c);
 }
 
 constexpr float kLog2e = 1.44269504f;
@@ -229,12 +237,14 @@ distill_rows_kernel(DistillArgs A, int C) {
   using V = Vec<T, 16>;
   constexpr int TEAMS = 256 / TEAM;
   constexpr bool AHEAD = TEAM != 32;         // load the next row early; other warps hide a warp's loads
-  __shared__ float2 red[2][8], stat[2];
-  __shared__ float probs_s[TEAMS * DISTILL_MAX_K];
+  __shared__ float2 red[2][8], stat[2][8];
+  // a team's probabilities and ids; a CTA's two sets are used in turn
+  constexpr int SETS = TEAM == 32 ? TEAMS : 2;
+  __shared__ float probs_s[SETS * DISTILL_MAX_K];
+  __shared__ int32_t ids_s[SETS * DISTILL_MAX_K];
   __shared__ int some_s[2];
   const int warp = threadIdx.x >> 5, r = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
-  float* probs = probs_s + (TEAM == 32 ? warp * DISTILL_MAX_K : 0);
   const float c = kLog2e / A.temperature;
   const int64_t step = (int64_t)gridDim.x / C * TEAMS;
   int64_t i = (int64_t)blockIdx.x / C * TEAMS + (TEAM == 32 ? warp : 0);
@@ -259,7 +269,10 @@ distill_rows_kernel(DistillArgs A, int C) {
     v[q].fill(kNegInf<T>);
     if (q * TEAM < nv) v[q].load(sv, q * TEAM);
   };
+  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
+  Teacher R, next;
   if (AHEAD) {
+    if (warp == 0) next = teacher_load<T>(A, i);
     enter(i);
 #pragma unroll
     for (int q = 0; q < NV; ++q) take(q);
@@ -272,9 +285,12 @@ distill_rows_kernel(DistillArgs A, int C) {
 #pragma unroll
       for (int q = 0; q < NV; ++q) take(q);
     }
-    Teacher R{false, -1, 0.0f, 0.0f};
+    const int set = (TEAM == 32 ? warp : turn) * DISTILL_MAX_K;
+    float* probs = probs_s + set;
+    int32_t* ids = ids_s + set;
     if (TEAM == 32 || warp == 0) {
-      R = teacher_row(A, i, probs);
+      R = AHEAD ? next : teacher_load<T>(A, i);
+      teacher_solve(A, i, R, probs, ids);
       if (TEAM != 32 && r == 0) some_s[turn] = R.some;
     }
     // four maxima and four sums side by side: one chain would wait for itself
@@ -308,24 +324,20 @@ distill_rows_kernel(DistillArgs A, int C) {
       __syncwarp();
     } else {
       float2 all = cta_join<256>(make_float2(m, z), c, red[turn]);
-      if (C > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
-        if (r == 0) stat[turn] = all;
-        cluster.sync();
-        all = *cluster.map_shared_rank(&stat[turn], 0);
-        for (int q = 1; q < C; ++q) all = join(all, *cluster.map_shared_rank(&stat[turn], q), c);
-      }
+      if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
       m = all.x;
       z = all.y;
       some = some_s[turn];
     }
-    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, R);
     const RowPart now = P;
     const int nv_now = nv;
     const float one_now = one;
     const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
     uint4* gv = reinterpret_cast<uint4*>(g + now.head) + now.v0 + r;
-    if (AHEAD) enter(i + step);
+    if (AHEAD) {
+      if (warp == 0) next = teacher_load<T>(A, i + step);
+      enter(i + step);
+    }
 #pragma unroll
     for (int q0 = 0; q0 < NV; q0 += 4) {
       if (g && some && q0 < used) {
@@ -348,16 +360,18 @@ distill_rows_kernel(DistillArgs A, int C) {
         for (int q = q0; q < q0 + 4 && q < NV; ++q) take(q);
       }
     }
+    if (g && now.has) g[now.single] = elem_from_f<T>(some ? exp2_fast((one_now - m) * c) * aiz : 0.0f);
+    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, ids, R);
     if (g) {
-      if (now.has) g[now.single] = elem_from_f<T>(some ? exp2_fast((one_now - m) * c) * aiz : 0.0f);
+      // the kept classes after all others; a CTA's next row uses the other sets,
+      // and its barrier there holds this row's readers together
       if (TEAM == 32) __syncwarp(); else __syncthreads();
       if (some) {
-        if (TEAM == 32 && A.k <= 32) kept_gradients_warp<T>(A, R, s, g, m, c, a, aiz, probs);
-        else kept_gradients<T>(A, r, TEAM, i, s, g, m, c, a, aiz, probs, now.lo, now.hi);
+        if (TEAM == 32 && A.k <= 32) kept_gradients_warp<T>(R, g, m, c, a, aiz, probs);
+        else kept_gradients<T>(A.k, r, TEAM, s, g, m, c, a, aiz, probs, ids, now.lo, now.hi);
       }
     }
-    // the next row's probabilities overwrite these
-    if (TEAM == 32) __syncwarp(); else __syncthreads();
+    if (TEAM == 32) __syncwarp();            // the next row's probabilities overwrite these
   }
   if (C > 1) cg::this_cluster().sync();      // no CTA ends while another reads its statistics
 }
@@ -369,21 +383,25 @@ template <typename T, int BYTES>
 __global__ void __launch_bounds__(DW_T, 2)
 distill_wide_kernel(DistillArgs A, int C) {
   using V = Vec<T, BYTES>;
-  __shared__ float2 red[2][DW_T / 32], stat[2];
-  __shared__ float probs[DISTILL_MAX_K];
+  __shared__ float2 red[2][DW_T / 32], stat[2][8];
+  __shared__ float probs_s[2][DISTILL_MAX_K];
+  __shared__ int32_t ids_s[2][DISTILL_MAX_K];
   __shared__ int some_s[2];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = C == 1 ? 0 : (int)cluster.block_rank(), t = threadIdx.x, warp = t >> 5;
+  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank(), t = threadIdx.x, warp = t >> 5;
   const float c = kLog2e / A.temperature;
+  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
   int turn = 0;
   for (int64_t i = blockIdx.x / C; i < A.n; i += gridDim.x / C, turn ^= 1) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
     const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
     const T* sv = s + P.head;
-    Teacher R{false, -1, 0.0f, 0.0f};
+    float* probs = probs_s[turn];
+    int32_t* ids = ids_s[turn];
+    Teacher R;
     if (warp == 0) {
-      R = teacher_row(A, i, probs);
+      R = teacher_load<T>(A, i);
+      teacher_solve(A, i, R, probs, ids);
       if (t == 0) some_s[turn] = R.some;
     }
     // running maximum and sum: the sum is rescaled once per four vectors
@@ -409,16 +427,11 @@ distill_wide_kernel(DistillArgs A, int C) {
           for (int e = 0; e < V::N; ++e) z += exp2_fast((v[u].get(e) - shift) * c);
     }
     float2 all = cta_join<DW_T>(make_float2(m, z), c, red[turn]);
-    if (C > 1) {
-      if (t == 0) stat[turn] = all;
-      cluster.sync();
-      all = *cluster.map_shared_rank(&stat[turn], 0);
-      for (int q = 1; q < C; ++q) all = join(all, *cluster.map_shared_rank(&stat[turn], q), c);
-    }
+    if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
     m = all.x;
     z = all.y;
     const bool some = some_s[turn];
-    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, R);
+    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, ids, R);
     if (g) {
       const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
       T* gv = g + P.head;
@@ -441,11 +454,10 @@ distill_wide_kernel(DistillArgs A, int C) {
       }
       if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((elem_to_f<T>(s[P.single]) - m) * c) * aiz : 0.0f);
       __syncthreads();
-      if (some) kept_gradients<T>(A, t, DW_T, i, s, g, m, c, a, aiz, probs, P.lo, P.hi);
+      if (some) kept_gradients<T>(A.k, t, DW_T, s, g, m, c, a, aiz, probs, ids, P.lo, P.hi);
     }
-    __syncthreads();
   }
-  if (C > 1) cluster.sync();
+  if (C > 1) cg::this_cluster().sync();
 }
 
 // `teams` of C CTAs, but no more than run at the same time: the CTAs of a cluster
