@@ -5,20 +5,19 @@
 // masks of the type's lowest value must not overflow.)
 //
 // Bound by memory: the logits are read once and the gradient is written once.
-// The row stays in registers between its statistics and its gradient, held by a
-// team: a warp (rows up to 16 KB, where there are rows enough to fill the GPU:
-// no barrier anywhere), a CTA of 256 threads (up to 64 KB), or a cluster of two
-// to eight such CTAs (up to 512 KB), which join their statistics through
-// distributed shared memory. A CTA goes from row to row, and as soon as a vector
-// of the gradient is written its register takes the next row's vector, so that
-// row's loads run under this row's stores and barriers. Longer rows are streamed twice, the second time
-// from L2, by clusters of eight. Warp 0 of a CTA works out the teacher's
-// probabilities while the row's loads are in flight. A row's 16-byte vectors
-// start wherever its address allows; up to 14 elements before and after them go
-// one by one.
+// Between its statistics and its gradient a row stays
+//   in the registers of a warp: rows up to 16 KB, where there are enough of them
+//     to fill the GPU; no barrier anywhere;
+//   in the shared memory of a CTA (parts up to 50 KB), or of a cluster of two to
+//     eight CTAs that join their statistics through distributed shared memory.
+//     Two stages: the next row's part is on its way from the start of this one.
+//     (In registers, with the next row's loads issued as the gradient frees them,
+//     777 rows of 400 KB took 191 us.)
+// Longer rows are streamed twice, the second time from L2, by clusters of eight.
+// Warp 0 of a CTA works out the teacher's probabilities beside the statistics. A
+// row's 16-byte vectors start wherever its address allows; up to 14 elements
+// before and after them go one by one.
 #include <cooperative_groups.h>
-
-#include <atomic>
 
 #include "nerf_experts.cuh"
 #include "nerf_vec.cuh"
@@ -40,6 +39,14 @@ struct DistillArgs {
   float* loss;
   void* grad;
 };
+
+__device__ __forceinline__ void copy_async16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // 2^x within 2^-22 of its value; 0 below the normal range
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -226,79 +233,40 @@ struct RowPart {
   }
 };
 
-// Rows in registers: NV vectors a thread and one single element. TEAM 32: a warp
-// a row, eight rows to a CTA; TEAM 256: a CTA, or a cluster of them, a row.
-constexpr int rows_per_sm(int team, int nv) {
-  return nv <= 2 ? 4 : nv <= 8 ? 3 : team == 32 && nv == 32 ? 1 : 2;
-}
-template <typename T, int TEAM, int NV>
-__global__ void __launch_bounds__(256, rows_per_sm(TEAM, NV))
-distill_rows_kernel(DistillArgs A, int C) {
+// Rows in registers: a warp a row, NV vectors a lane and one single element.
+constexpr int rows_per_sm(int nv) { return nv <= 2 ? 4 : nv <= 8 ? 3 : nv <= 16 ? 2 : 1; }
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, rows_per_sm(NV))
+distill_rows_kernel(DistillArgs A) {
   using V = Vec<T, 16>;
-  constexpr int TEAMS = 256 / TEAM;
-  constexpr bool AHEAD = TEAM != 32;         // load the next row early; other warps hide a warp's loads
-  __shared__ float2 red[2][8], stat[2][8];
-  // a team's probabilities and ids; a CTA's two sets are used in turn
-  constexpr int SETS = TEAM == 32 ? TEAMS : 2;
-  __shared__ float probs_s[SETS * DISTILL_MAX_K];
-  __shared__ int32_t ids_s[SETS * DISTILL_MAX_K];
-  __shared__ int some_s[2];
-  const int warp = threadIdx.x >> 5, r = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  __shared__ float probs_s[8][DISTILL_MAX_K];
+  __shared__ int32_t ids_s[8][DISTILL_MAX_K];
+  const int warp = threadIdx.x >> 5, r = threadIdx.x & 31;
+  float* probs = probs_s[warp];
+  int32_t* ids = ids_s[warp];
   const float c = kLog2e / A.temperature;
-  const int64_t step = (int64_t)gridDim.x / C * TEAMS;
-  int64_t i = (int64_t)blockIdx.x / C * TEAMS + (TEAM == 32 ? warp : 0);
-  V v[NV];
-  RowPart P;
-  const uint4* sv;
-  int nv;                                    // this thread's vectors: q * TEAM < nv
-  float one;
-  // row i's part and its vectors' place; the loads are issued by the caller
-  auto enter = [&](int64_t row) {
-    const bool in = row < A.n;
-    const T* s = (const T*)A.student + (in ? row : 0) * A.classes;
-    P = RowPart::of<T, V::N>(s, A.classes, rank, C, r);
-    P.has = P.has && in;
-    sv = reinterpret_cast<const uint4*>(s + P.head) + P.v0 + r;
-    nv = in ? P.v1 - P.v0 - r : 0;
-    one = P.has ? elem_to_f<T>(s[P.single]) : -INFINITY;
-  };
-  // a vector past the part holds -inf: it adds nothing to the statistics, which
-  // are then free of conditions
-  auto take = [&](int q) {
-    v[q].fill(kNegInf<T>);
-    if (q * TEAM < nv) v[q].load(sv, q * TEAM);
-  };
-  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
-  Teacher R, next;
-  if (AHEAD) {
-    if (warp == 0) next = teacher_load<T>(A, i);
-    enter(i);
-#pragma unroll
-    for (int q = 0; q < NV; ++q) take(q);
-  }
-  for (int turn = 0; i < A.n; i += step, turn ^= 1) {
+  for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < A.n; i += (int64_t)gridDim.x * 8) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
-    if (!AHEAD) {
-      enter(i);
+    const RowPart P = RowPart::of<T, V::N>(s, A.classes, 0, 1, r);
+    const T* sv = s + P.head;
+    const int nv = P.v1 - r;                 // this lane's vectors: q * 32 < nv
+    // a vector past the row holds -inf and adds nothing to the statistics
+    V v[NV];
 #pragma unroll
-      for (int q = 0; q < NV; ++q) take(q);
+    for (int q = 0; q < NV; ++q) {
+      v[q].fill(kNegInf<T>);
+      if (q * 32 < nv) v[q].load(sv, r + q * 32);
     }
-    const int set = (TEAM == 32 ? warp : turn) * DISTILL_MAX_K;
-    float* probs = probs_s + set;
-    int32_t* ids = ids_s + set;
-    if (TEAM == 32 || warp == 0) {
-      R = AHEAD ? next : teacher_load<T>(A, i);
-      teacher_solve(A, i, R, probs, ids);
-      if (TEAM != 32 && r == 0) some_s[turn] = R.some;
-    }
-    // four maxima and four sums side by side: one chain would wait for itself
-    float mp[4] = {one, one, one, one};
+    const float one = P.has ? elem_to_f<T>(s[P.single]) : -INFINITY;
+    Teacher R = teacher_load<T>(A, i);
+    teacher_solve(A, i, R, probs, ids);
     // The passes go over groups of four vectors, each behind a condition that the
-    // whole team shares: unused groups are skipped, and a row of 16-bit elements is
-    // never unpacked as a whole, which would not fit the registers.
-    const int used = (P.v1 - P.v0 + TEAM - 1) / TEAM;
+    // warp shares: unused groups are skipped, and a row of 16-bit elements is never
+    // unpacked as a whole, which would not fit the registers. Four maxima and four
+    // sums run side by side: one chain would wait for itself.
+    const int used = (P.v1 + 31) / 32;
+    float mp[4] = {one, one, one, one};
 #pragma unroll
     for (int q0 = 0; q0 < NV; q0 += 4)
       if (q0 < used)
@@ -306,74 +274,147 @@ distill_rows_kernel(DistillArgs A, int C) {
         for (int q = q0; q < q0 + 4 && q < NV; ++q)
 #pragma unroll
           for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], v[q].get(e));
-    float m = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
-    if (TEAM == 32) m = warp_max(m);
-    const float shift = TEAM != 32 && m == -INFINITY ? 0.0f : m;
-    float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
+    const float m = warp_max(max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3])));
+    float zp[4] = {exp2_fast((one - m) * c), 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int q0 = 0; q0 < NV; q0 += 4)
       if (q0 < used)
 #pragma unroll
         for (int q = q0; q < q0 + 4 && q < NV; ++q)
 #pragma unroll
-          for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((v[q].get(e) - shift) * c);
-    float z = (zp[0] + zp[1]) + (zp[2] + zp[3]);
-    bool some = R.some;
-    if (TEAM == 32) {
-      z = warp_sum(z);
-      __syncwarp();
-    } else {
-      float2 all = cta_join<256>(make_float2(m, z), c, red[turn]);
-      if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
-      m = all.x;
-      z = all.y;
-      some = some_s[turn];
-    }
-    const RowPart now = P;
-    const int nv_now = nv;
-    const float one_now = one;
+          for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((v[q].get(e) - m) * c);
+    const float z = warp_sum((zp[0] + zp[1]) + (zp[2] + zp[3]));
     const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
-    uint4* gv = reinterpret_cast<uint4*>(g + now.head) + now.v0 + r;
-    if (AHEAD) {
-      if (warp == 0) next = teacher_load<T>(A, i + step);
-      enter(i + step);
-    }
-#pragma unroll
-    for (int q0 = 0; q0 < NV; q0 += 4) {
-      if (g && some && q0 < used) {
-#pragma unroll
-        for (int q = q0; q < q0 + 4 && q < NV; ++q) {
-          float f[V::N];
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) f[e] = exp2_fast((v[q].get(e) - m) * c) * aiz;
-          V o;
-          o.pack(f);
-          if (q * TEAM < nv_now) o.store(gv, q * TEAM);
-        }
-      } else if (g && q0 < used) {
-#pragma unroll
-        for (int q = q0; q < q0 + 4 && q < NV; ++q)
-          if (q * TEAM < nv_now) gv[q * TEAM] = make_uint4(0, 0, 0, 0);
-      }
-      if (AHEAD) {
-#pragma unroll
-        for (int q = q0; q < q0 + 4 && q < NV; ++q) take(q);
-      }
-    }
-    if (g && now.has) g[now.single] = elem_from_f<T>(some ? exp2_fast((one_now - m) * c) * aiz : 0.0f);
-    if ((TEAM == 32 || warp == 0) && rank == 0) write_loss<T>(A, i, s, m, z, probs, ids, R);
     if (g) {
-      // the kept classes after all others; a CTA's next row uses the other sets,
-      // and its barrier there holds this row's readers together
-      if (TEAM == 32) __syncwarp(); else __syncthreads();
-      if (some) {
-        if (TEAM == 32 && A.k <= 32) kept_gradients_warp<T>(R, g, m, c, a, aiz, probs);
-        else kept_gradients<T>(A.k, r, TEAM, s, g, m, c, a, aiz, probs, ids, now.lo, now.hi);
+      T* gv = g + P.head;
+#pragma unroll
+      for (int q0 = 0; q0 < NV; q0 += 4) {
+        if (R.some && q0 < used) {
+#pragma unroll
+          for (int q = q0; q < q0 + 4 && q < NV; ++q) {
+            float f[V::N];
+#pragma unroll
+            for (int e = 0; e < V::N; ++e) f[e] = exp2_fast((v[q].get(e) - m) * c) * aiz;
+            V o;
+            o.pack(f);
+            if (q * 32 < nv) o.store(gv, r + q * 32);
+          }
+        } else if (q0 < used) {
+          V o;
+          o.fill(0);
+#pragma unroll
+          for (int q = q0; q < q0 + 4 && q < NV; ++q)
+            if (q * 32 < nv) o.store(gv, r + q * 32);
+        }
       }
+      if (P.has) g[P.single] = elem_from_f<T>(R.some ? exp2_fast((one - m) * c) * aiz : 0.0f);
     }
-    if (TEAM == 32) __syncwarp();            // the next row's probabilities overwrite these
+    write_loss<T>(A, i, s, m, z, probs, ids, R);
+    __syncwarp();                            // the kept classes after all others
+    if (g && R.some) {
+      if (A.k <= 32) kept_gradients_warp<T>(R, g, m, c, a, aiz, probs);
+      else kept_gradients<T>(A.k, r, 32, s, g, m, c, a, aiz, probs, ids, 0, A.classes);
+    }
+    __syncwarp();                            // the next row's probabilities overwrite these
   }
-  if (C > 1) cg::this_cluster().sync();      // no CTA ends while another reads its statistics
+}
+
+// Rows in shared memory: a CTA, or a cluster of C of them, a row. A thread copies,
+// reads and rewrites only vectors of its own, so the stages need no barrier.
+constexpr int DS_T = 512;
+constexpr int DS_PART = 50 * 1024;           // bytes of a part: two stages for each of two CTAs fit an SM
+template <typename T>
+__global__ void __launch_bounds__(DS_T, 2)
+distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
+  using V = Vec<T, 16>;
+  extern __shared__ uint4 stages[];          // [2][stage_vecs]
+  __shared__ float2 red[2][DS_T / 32], stat[2][8];
+  __shared__ float probs_s[2][DISTILL_MAX_K];   // two sets, used in turn
+  __shared__ int32_t ids_s[2][DISTILL_MAX_K];
+  __shared__ int some_s[2];
+  const int t = threadIdx.x, warp = t >> 5, rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  const float c = kLog2e / A.temperature;
+  const int64_t step = gridDim.x / C;
+  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
+  Teacher R, next;
+  RowPart P, Pn;
+  float one, one_next;
+  int64_t i = blockIdx.x / C;
+  // starts the copies of row `row` (none past the last) into a stage
+  auto fetch = [&](int64_t row, int stage) {
+    one_next = -INFINITY;
+    if (row < A.n) {
+      const T* s = (const T*)A.student + row * A.classes;
+      Pn = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
+      const uint4* sv = reinterpret_cast<const uint4*>(s + Pn.head) + Pn.v0;
+      for (int q = t; q < Pn.v1 - Pn.v0; q += DS_T) copy_async16(&stages[stage * stage_vecs + q], sv + q);
+      if (Pn.has) one_next = elem_to_f<T>(s[Pn.single]);
+      if (warp == 0) next = teacher_load<T>(A, row);
+    }
+    copy_commit();
+  };
+  fetch(i, 0);
+  for (int turn = 0; i < A.n; i += step, turn ^= 1) {
+    P = Pn;
+    one = one_next;
+    R = next;
+    fetch(i + step, turn ^ 1);
+    const T* s = (const T*)A.student + i * A.classes;
+    T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
+    float* probs = probs_s[turn];
+    int32_t* ids = ids_s[turn];
+    if (warp == 0) {
+      teacher_solve(A, i, R, probs, ids);
+      if (t == 0) some_s[turn] = R.some;
+    }
+    const uint4* v = stages + turn * stage_vecs;
+    const int nv = P.v1 - P.v0;
+    copy_wait<1>();                          // this row's copies; the next row's may still run
+    float mp[4] = {one, one, one, one};
+#pragma unroll 2
+    for (int q = t; q < nv; q += DS_T) {
+      const V x = V::of(v[q]);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], x.get(e));
+    }
+    const float top = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+    for (int q = t; q < nv; q += DS_T) {
+      const V x = V::of(v[q]);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((x.get(e) - shift) * c);
+    }
+    float2 all = cta_join<DS_T>(make_float2(top, (zp[0] + zp[1]) + (zp[2] + zp[3])), c, red[turn]);
+    if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
+    const float m = all.x, z = all.y;
+    const bool some = some_s[turn];
+    const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
+    if (g) {
+      T* gv = g + P.head;
+#pragma unroll 2
+      for (int q = t; q < nv; q += DS_T) {
+        const V x = V::of(v[q]);
+        float f[V::N];
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) f[e] = some ? exp2_fast((x.get(e) - m) * c) * aiz : 0.0f;
+        V o;
+        o.pack(f);
+        o.store(gv, P.v0 + q);
+      }
+      if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((one - m) * c) * aiz : 0.0f);
+    }
+    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, ids, R);
+    if (g) {
+      // the kept classes after all others. The next row uses the other sets, and its
+      // barrier holds this row's readers together.
+      __syncthreads();
+      if (some) kept_gradients<T>(A.k, t, DS_T, s, g, m, c, a, aiz, probs, ids, P.lo, P.hi);
+    }
+  }
+  copy_wait<0>();
+  if (C > 1) cg::this_cluster().sync();      // no CTA ends while another writes to it
 }
 
 // Long rows, or rows whose gradient is aligned unlike them (BYTES = one
@@ -463,10 +504,11 @@ distill_wide_kernel(DistillArgs A, int C) {
 // `teams` of C CTAs, but no more than run at the same time: the CTAs of a cluster
 // share a GPC, whose SMs a size of eight does not divide, so fewer clusters fit
 // than SMs x CTAs / C, and a last few started late would run alone.
-template <typename K>
-cudaError_t run_clusters(K kernel, const DistillArgs& A, int64_t teams, int threads, int C, cudaStream_t st) {
+template <typename K, typename... Args>
+cudaError_t run_clusters(K kernel, int64_t teams, int threads, size_t smem, int C, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -474,28 +516,33 @@ cudaError_t run_clusters(K kernel, const DistillArgs& A, int64_t teams, int thre
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  if (C > 1 && teams > 1) {
-    static std::atomic<int> fit[4] = {};     // of this kernel, by log2 C; the same on every device (sm_100a)
-    std::atomic<int>& f = fit[C == 2 ? 1 : C == 4 ? 2 : 3];
-    int most = f.load(std::memory_order_relaxed);
-    if (most == 0) {
-      cfg.gridDim = dim3((unsigned)C);
-      const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      if (most < 1) most = 1;
-      f.store(most, std::memory_order_relaxed);
-    }
-    if (teams > most) teams = most;
-  }
   cfg.gridDim = dim3((unsigned)(teams * C));
-  return cudaLaunchKernelEx(&cfg, kernel, A, C);
+  if (C > 1 && teams * C > 148) {
+    int most = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (most >= 1 && teams > most) cfg.gridDim = dim3((unsigned)most * C);
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int TEAM, int NV>
-cudaError_t run_rows(const DistillArgs& A, int C, cudaStream_t st) {
-  constexpr int TEAMS = 256 / TEAM;
-  const int64_t want = (A.n + TEAMS - 1) / TEAMS, most = 148 * rows_per_sm(TEAM, NV) / C;
-  return run_clusters(distill_rows_kernel<T, TEAM, NV>, A, want < most ? want : most, 256, C, st);
+template <typename T, int NV>
+cudaError_t run_rows(const DistillArgs& A, cudaStream_t st) {
+  const int64_t want = (A.n + 7) / 8, most = 148 * rows_per_sm(NV);
+  distill_rows_kernel<T, NV><<<(unsigned)(want < most ? want : most), 256, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_stage(const DistillArgs& A, int C, cudaStream_t st) {
+  const int64_t bytes = (int64_t)A.classes * sizeof(T);
+  const int vecs = (int)((bytes / 16 + C - 1) / C) + 1;
+  const size_t smem = (size_t)vecs * 32;
+  const cudaError_t e = cudaFuncSetAttribute(distill_stage_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             2 * DS_PART + 64);
+  if (e != cudaSuccess) return e;
+  const int64_t most = 296 / C;
+  return run_clusters(distill_stage_kernel<T>, A.n < most ? A.n : most, DS_T, smem, C, st, A, C, vecs);
 }
 
 template <typename T, int BYTES>
@@ -506,7 +553,7 @@ cudaError_t run_wide(const DistillArgs& A, cudaStream_t st) {
   int C = 8;
   while (C > 1 && bytes / C < 32768) C /= 2;
   const int64_t most = 296 / C;
-  return run_clusters(distill_wide_kernel<T, BYTES>, A, A.n < most ? A.n : most, DW_T, C, st);
+  return run_clusters(distill_wide_kernel<T, BYTES>, A.n < most ? A.n : most, DW_T, 0, C, st, A, C);
 }
 
 template <typename T>
@@ -514,19 +561,15 @@ cudaError_t run_t(const DistillArgs& A, cudaStream_t st) {
   const int64_t bytes = (int64_t)A.classes * sizeof(T);
   // the vectors of student and gradient rows coincide when both start alike
   if (A.grad && ((uintptr_t)A.grad - (uintptr_t)A.student) % 16) return run_wide<T, (int)sizeof(T)>(A, st);
-  if (bytes <= 512) return run_rows<T, 32, 1>(A, 1, st);
-  if (bytes <= 1024) return run_rows<T, 32, 2>(A, 1, st);
-  if (bytes <= 4096) return run_rows<T, 32, 8>(A, 1, st);
+  if (bytes <= 512) return run_rows<T, 1>(A, st);
+  if (bytes <= 1024) return run_rows<T, 2>(A, st);
+  if (bytes <= 4096) return run_rows<T, 8>(A, st);
   // a warp a row needs some 1200 rows to fill the SMs
-  if (A.n >= 1184 && bytes <= 8192) return run_rows<T, 32, 16>(A, 1, st);
-  if (A.n >= 1184 && bytes <= 16384) return run_rows<T, 32, 32>(A, 1, st);
-  if (bytes <= 16384) return run_rows<T, 256, 4>(A, 1, st);
-  int C = 1;                                 // CTAs of a row: parts of 64 KB at most
-  while (bytes > 65536 * (int64_t)C) C *= 2;
-  if (C > 8) return run_wide<T, 16>(A, st);
-  const int64_t part = (bytes + C - 1) / C + 16;
-  if (part <= 32768) return run_rows<T, 256, 8>(A, C, st);
-  return run_rows<T, 256, 16>(A, C, st);
+  if (A.n >= 1184 && bytes <= 8192) return run_rows<T, 16>(A, st);
+  if (A.n >= 1184 && bytes <= 16384) return run_rows<T, 32>(A, st);
+  int C = 1;                                 // CTAs of a row
+  while (C <= 8 && bytes > (int64_t)DS_PART * C) C *= 2;
+  return C <= 8 ? run_stage<T>(A, C, st) : run_wide<T, 16>(A, st);
 }
 
 }  // namespace

@@ -66,6 +66,12 @@ struct Vec {
     else
       reinterpret_cast<uint16_t*>(p)[v] = (uint16_t)words[0];
   }
+  static __device__ __forceinline__ Vec of(const uint4& r) {
+    static_assert(BYTES == 16, "a whole vector");
+    Vec v;
+    v.words[0] = r.x, v.words[1 % W] = r.y, v.words[2 % W] = r.z, v.words[3 % W] = r.w;
+    return v;
+  }
   __device__ __forceinline__ void fill(uint32_t w) {
 #pragma unroll
     for (int i = 0; i < W; ++i) words[i] = w;
