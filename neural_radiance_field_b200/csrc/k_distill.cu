@@ -319,9 +319,14 @@ distill_rows_kernel(DistillArgs A) {
   }
 }
 
-// Rows in shared memory: a CTA, or a cluster of C of them, a row. A thread copies,
-// reads and rewrites only vectors of its own, so the stages need no barrier.
-constexpr int DS_T = 512;
+// Rows in shared memory: a CTA, or a cluster of C of them, a row. Fifteen warps
+// work on the row; a thread copies, reads and rewrites only vectors of its own,
+// so the stages need no barrier. The last warp has the teacher: it solves a row's
+// probabilities while the others take its statistics, writes the loss, and
+// corrects the kept classes once the others have written theirs, for which they
+// arrive at a barrier without waiting. (On warp 0 that work, a chain of dependent
+// loads, held the CTA up for half of the time: 195 us at 777 rows of 400 KB where this takes 151.)
+constexpr int DS_T = 512, DS_M = DS_T - 32;
 constexpr int DS_PART = 50 * 1024;           // bytes of a part: two stages for each of two CTAs fit an SM
 template <typename T>
 __global__ void __launch_bounds__(DS_T, 2)
@@ -329,91 +334,99 @@ distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
   using V = Vec<T, 16>;
   extern __shared__ uint4 stages[];          // [2][stage_vecs]
   __shared__ float2 red[2][DS_T / 32], stat[2][8];
-  __shared__ float probs_s[2][DISTILL_MAX_K];   // two sets, used in turn
-  __shared__ int32_t ids_s[2][DISTILL_MAX_K];
+  __shared__ float probs[DISTILL_MAX_K];     // of the last warp alone
+  __shared__ int32_t ids[DISTILL_MAX_K];
   __shared__ int some_s[2];
-  const int t = threadIdx.x, warp = t >> 5, rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  const int t = threadIdx.x, rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  const bool teacher = t >= DS_M;
   const float c = kLog2e / A.temperature;
   const int64_t step = gridDim.x / C;
-  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
-  Teacher R, next;
-  RowPart P, Pn;
-  float one, one_next;
   int64_t i = blockIdx.x / C;
-  // starts the copies of row `row` (none past the last) into a stage
-  auto fetch = [&](int64_t row, int stage) {
-    one_next = -INFINITY;
-    if (row < A.n) {
-      const T* s = (const T*)A.student + row * A.classes;
-      Pn = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
-      const uint4* sv = reinterpret_cast<const uint4*>(s + Pn.head) + Pn.v0;
-      for (int q = t; q < Pn.v1 - Pn.v0; q += DS_T) copy_async16(&stages[stage * stage_vecs + q], sv + q);
-      if (Pn.has) one_next = elem_to_f<T>(s[Pn.single]);
-      if (warp == 0) next = teacher_load<T>(A, row);
-    }
-    copy_commit();
-  };
-  fetch(i, 0);
-  for (int turn = 0; i < A.n; i += step, turn ^= 1) {
-    P = Pn;
-    one = one_next;
-    R = next;
-    fetch(i + step, turn ^ 1);
-    const T* s = (const T*)A.student + i * A.classes;
-    T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
-    float* probs = probs_s[turn];
-    int32_t* ids = ids_s[turn];
-    if (warp == 0) {
+  if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
+  if (teacher) {
+    Teacher R = teacher_load<T>(A, i);
+    for (int turn = 0; i < A.n; i += step, turn ^= 1) {
+      const T* s = (const T*)A.student + i * A.classes;
+      T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
       teacher_solve(A, i, R, probs, ids);
-      if (t == 0) some_s[turn] = R.some;
-    }
-    const uint4* v = stages + turn * stage_vecs;
-    const int nv = P.v1 - P.v0;
-    copy_wait<1>();                          // this row's copies; the next row's may still run
-    float mp[4] = {one, one, one, one};
-#pragma unroll 2
-    for (int q = t; q < nv; q += DS_T) {
-      const V x = V::of(v[q]);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], x.get(e));
-    }
-    const float top = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
-    const float shift = top == -INFINITY ? 0.0f : top;
-    float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-    for (int q = t; q < nv; q += DS_T) {
-      const V x = V::of(v[q]);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((x.get(e) - shift) * c);
-    }
-    float2 all = cta_join<DS_T>(make_float2(top, (zp[0] + zp[1]) + (zp[2] + zp[3])), c, red[turn]);
-    if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
-    const float m = all.x, z = all.y;
-    const bool some = some_s[turn];
-    const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
-    if (g) {
-      T* gv = g + P.head;
-#pragma unroll 2
-      for (int q = t; q < nv; q += DS_T) {
-        const V x = V::of(v[q]);
-        float f[V::N];
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) f[e] = some ? exp2_fast((x.get(e) - m) * c) * aiz : 0.0f;
-        V o;
-        o.pack(f);
-        o.store(gv, P.v0 + q);
+      if (t == DS_M) some_s[turn] = R.some;
+      __syncwarp();
+      float2 all = cta_join<DS_T>(make_float2(-INFINITY, 0.0f), c, red[turn]);
+      if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
+      const Teacher now = R;
+      R = teacher_load<T>(A, i + step);
+      if (rank == 0) write_loss<T>(A, i, s, all.x, all.y, probs, ids, now);
+      if (g) {
+        asm volatile("bar.sync 1, %0;" ::"n"(DS_T) : "memory");
+        const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f);
+        const RowPart P = RowPart::of<T, V::N>(s, A.classes, rank, C, 0);
+        if (now.some) kept_gradients<T>(A.k, t - DS_M, 32, s, g, all.x, c, a, a / all.y, probs, ids, P.lo, P.hi);
       }
-      if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((one - m) * c) * aiz : 0.0f);
+      __syncwarp();                          // the next row's probabilities overwrite these
     }
-    if (warp == 0 && rank == 0) write_loss<T>(A, i, s, m, z, probs, ids, R);
-    if (g) {
-      // the kept classes after all others. The next row uses the other sets, and its
-      // barrier holds this row's readers together.
-      __syncthreads();
-      if (some) kept_gradients<T>(A.k, t, DS_T, s, g, m, c, a, aiz, probs, ids, P.lo, P.hi);
+  } else {
+    RowPart P, Pn;
+    float one, one_next;
+    // starts the copies of row `row` (none past the last) into a stage
+    auto fetch = [&](int64_t row, int stage) {
+      one_next = -INFINITY;
+      if (row < A.n) {
+        const T* s = (const T*)A.student + row * A.classes;
+        Pn = RowPart::of<T, V::N>(s, A.classes, rank, C, t);
+        const uint4* sv = reinterpret_cast<const uint4*>(s + Pn.head) + Pn.v0;
+        for (int q = t; q < Pn.v1 - Pn.v0; q += DS_M) copy_async16(&stages[stage * stage_vecs + q], sv + q);
+        if (Pn.has) one_next = elem_to_f<T>(s[Pn.single]);
+      }
+      copy_commit();
+    };
+    fetch(i, 0);
+    for (int turn = 0; i < A.n; i += step, turn ^= 1) {
+      P = Pn;
+      one = one_next;
+      fetch(i + step, turn ^ 1);
+      T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
+      const uint4* v = stages + turn * stage_vecs;
+      const int nv = P.v1 - P.v0;
+      const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f);
+      copy_wait<1>();                        // this row's copies; the next row's may still run
+      float mp[4] = {one, one, one, one};
+#pragma unroll 2
+      for (int q = t; q < nv; q += DS_M) {
+        const V x = V::of(v[q]);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], x.get(e));
+      }
+      const float top = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
+      const float shift = top == -INFINITY ? 0.0f : top;
+      float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+      for (int q = t; q < nv; q += DS_M) {
+        const V x = V::of(v[q]);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((x.get(e) - shift) * c);
+      }
+      float2 all = cta_join<DS_T>(make_float2(top, (zp[0] + zp[1]) + (zp[2] + zp[3])), c, red[turn]);
+      if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
+      const float m = all.x, aiz = a / all.y;
+      const bool some = some_s[turn];
+      if (g) {
+        T* gv = g + P.head;
+#pragma unroll 2
+        for (int q = t; q < nv; q += DS_M) {
+          const V x = V::of(v[q]);
+          float f[V::N];
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) f[e] = some ? exp2_fast((x.get(e) - m) * c) * aiz : 0.0f;
+          V o;
+          o.pack(f);
+          o.store(gv, P.v0 + q);
+        }
+        if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((one - m) * c) * aiz : 0.0f);
+        asm volatile("bar.arrive 1, %0;" ::"n"(DS_T) : "memory");
+      }
     }
+    copy_wait<0>();
   }
-  copy_wait<0>();
   if (C > 1) cg::this_cluster().sync();      // no CTA ends while another writes to it
 }
 
