@@ -40,25 +40,17 @@ __device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(__fsub_rn(v, __uint_as_float(hi)));
 }
-__device__ __noinline__ float2 sincos_pi_far(float v) {
-  float2 r;
-  sincospif(v, &r.x, &r.y);
-  return r;
-}
 // sin and cos of pi v: v = n / 2 + r exactly, |r| <= 1/4, and two polynomials in
 // r^2 whose coefficients were fitted to sin(pi r) / r and cos(pi r) on that
-// interval by reweighted least squares. Within 1.5 * 2^-24 of the value over
-// |v| <= 384; 20 operations, two fifths fewer than the library call.
+// interval by reweighted least squares. Within 1.5 * 2^-24 of the value. A float
+// of 2^24 or more is an even number (or infinite, whose difference from itself is
+// NaN). Two fifths fewer operations than the library call, and no branch: a call
+// in these loops would take registers that they need.
 __device__ __forceinline__ void sincos_pi(float v, float* s, float* c) {
-  if (fabsf(v) > 1048576.0f) {               // the quadrant would not fit the mantissa
-    const float2 f = sincos_pi_far(v);
-    *s = f.x;
-    *c = f.y;
-    return;
-  }
-  const float t = fmaf(v, 2.0f, 12582912.0f);
-  const unsigned n = __float_as_uint(t);
-  const float r = fmaf(t - 12582912.0f, -0.5f, v), q = r * r;
+  if (!(fabsf(v) < 16777216.0f)) v -= v;
+  const float t = rintf(v + v);
+  const unsigned n = (unsigned)(int)t;
+  const float r = fmaf(t, -0.5f, v), q = r * r;
   const float a = r * fmaf(fmaf(fmaf(-5.890786648e-01f, q, 2.549767256f), q, -5.167707920f), q, 3.141592741f);
   const float b = fmaf(fmaf(fmaf(fmaf(2.314295471e-01f, q, -1.335058451f), q, 4.058707905f), q, -4.934802055f), q, 1.0f);
   const float p = n & 1 ? b : a, o = n & 1 ? a : b;
@@ -493,20 +485,18 @@ __device__ __forceinline__ void fetch_tile(BackwardTile& T, int lane, const floa
   copy_commit();
 }
 
-// c[u][m] = sum over the row halves q of z[q][m] b[u][q], for two column pairs u
-// and the two fragments m of 32 outputs
-__device__ __forceinline__ void weight_products(float (&c)[2][2][4], const uint32_t (&zh)[2][2][4],
-                                                const uint32_t (&zl)[2][2][4], const uint32_t (&bh)[2][2][2],
-                                                const uint32_t (&bl)[2][2][2]) {
+// c[u][m] = z[m] b[u] for two column pairs u and the two fragments m of 32
+// outputs; the three products of an accumulator stand four instructions apart
+__device__ __forceinline__ void weight_products(float (&c)[2][2][4], const uint32_t (&zh)[2][4],
+                                                const uint32_t (&zl)[2][4], const uint32_t (&bh)[2][2],
+                                                const uint32_t (&bl)[2][2]) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
+  for (int p = 0; p < 3; ++p)
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          mma_from(q == 0 && p == 0, c[u][m], p == 0 ? zl[q][m] : zh[q][m], p == 1 ? bl[u][q] : bh[u][q]);
+      for (int m = 0; m < 2; ++m)
+        mma_from(p == 0, c[u][m], p == 0 ? zl[m] : zh[m], p == 1 ? bl[u] : bh[u]);
 }
 
 struct CellsBackwardArgs {
@@ -552,90 +542,80 @@ __device__ __forceinline__ void backward_w1(const CellsBackwardArgs& P, CellsBac
     }
     __syncwarp();
     const BackwardTile& T = S.tile[warp][stage];
-    // g2 as operand B: features 8t .. 8t + 7 of rows g and g + 8; then g1 = (W2^T g2) (h1 > 0)
-    float dz[2][2][4];                       // [rows 0-7, 8-15][m tile]
-    float4 gr[2];
-    float mask[2][8];
+    // Eight rows at a time, in a loop that is not unrolled: with sixteen in
+    // straight line the two roles' code overran the instruction cache.
+#pragma unroll 1
+    for (int q = 0; q < CB_ROWS; q += 8) {
+      asm volatile("" ::: "memory");         // the weights' fragments are read anew, not held in registers
+      // g2 as operand B: features 8t .. 8t + 7 of row g; then g1 = (W2^T g2) (h1 > 0)
+      const float4 gr = T.d_raw[q + g];
+      const float4 m0 = *reinterpret_cast<const float4*>(&T.hidden[q + g][32 + 8 * t]);
+      const float4 m1 = *reinterpret_cast<const float4*>(&T.hidden[q + g][36 + 8 * t]);
+      const float mask[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+      float dz[2][2][4];                     // [k steps 0, 2 and 1, 3][m tile]
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      gr[q] = T.d_raw[8 * q + g];
-      const float4 m0 = *reinterpret_cast<const float4*>(&T.hidden[8 * q + g][32 + 8 * t]);
-      const float4 m1 = *reinterpret_cast<const float4*>(&T.hidden[8 * q + g][36 + 8 * t]);
-      mask[q][0] = m0.x, mask[q][1] = m0.y, mask[q][2] = m0.z, mask[q][3] = m0.w;
-      mask[q][4] = m1.x, mask[q][5] = m1.y, mask[q][6] = m1.z, mask[q][7] = m1.w;
-    }
+      for (int s = 0; s < 4; ++s) {
+        uint32_t bh[2], bl[2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const float4 w0 = S.wh[warp][8 * t + 2 * s], w1 = S.wh[warp][8 * t + 2 * s + 1];
-      uint32_t bh[2][2], bl[2][2];
+        for (int i = 0; i < 2; ++i)
+          split3(mask[2 * s + i] > 0.0f ? head_grad(S.wh[warp][8 * t + 2 * s + i], gr) : 0.0f, bh[i], bl[i]);
+        uint32_t wh[2][4], wl[2][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        split3(mask[q][2 * s] > 0.0f ? head_grad(w0, gr[q]) : 0.0f, bh[q][0], bl[q][0]);
-        split3(mask[q][2 * s + 1] > 0.0f ? head_grad(w1, gr[q]) : 0.0f, bh[q][1], bl[q][1]);
+        for (int m = 0; m < 2; ++m) {
+          const uint4 hi = S.hi[warp][(m * 4 + s) * 32 + lane], lo = S.lo[warp][(m * 4 + s) * 32 + lane];
+          wh[m][0] = hi.x, wh[m][1] = hi.y, wh[m][2] = hi.z, wh[m][3] = hi.w;
+          wl[m][0] = lo.x, wl[m][1] = lo.y, wl[m][2] = lo.z, wl[m][3] = lo.w;
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            mma_from(s < 2 && p == 0, dz[s & 1][m], p == 0 ? wl[m] : wh[m], p == 1 ? bl : bh);
       }
-      uint32_t wh[2][4], wl[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint4 hi = S.hi[warp][(m * 4 + s) * 32 + lane], lo = S.lo[warp][(m * 4 + s) * 32 + lane];
-        wh[m][0] = hi.x, wh[m][1] = hi.y, wh[m][2] = hi.z, wh[m][3] = hi.w;
-        wl[m][0] = lo.x, wl[m][1] = lo.y, wl[m][2] = lo.z, wl[m][3] = lo.w;
-      }
-      // the three products of an accumulator stand four instructions apart, here and below
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            mma_from(s == 0 && p == 0, dz[q][m], p == 0 ? wl[m] : wh[m], p == 1 ? bl[q] : bh[q]);
-    }
-    // C's (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1) are A's (g, t), (g, t+4), (g+8, t), (g+8, t+4)
-    uint32_t zh[2][2][4], zl[2][2][4];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
+      // C's (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1) are A's (g, t), (g, t+4), (g+8, t), (g+8, t+4)
+      uint32_t zh[2][4], zl[2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          split3(T.hidden[8 * q + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] > 0.0f ? dz[q][m][i] : 0.0f,
-                 zh[q][m][(i & 1) * 2 + (i >> 1)], zl[q][m][(i & 1) * 2 + (i >> 1)]);
+          split3(T.hidden[q + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] > 0.0f ? dz[0][m][i] + dz[1][m][i] : 0.0f,
+                 zh[m][(i & 1) * 2 + (i >> 1)], zl[m][(i & 1) * 2 + (i >> 1)]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float e[2][2][4];
+      for (int j = 0; j < 2; ++j) {
+        float e[2][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+        for (int i = 0; i < 2; ++i) (j ? base1 : base0).encode(&T.v[3 * (q + 2 * t + i)], 1.0f, e[i]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) (j ? base1 : base0).encode(&T.v[3 * (8 * q + 2 * t + i)], 1.0f, e[q][i]);
+        for (int i = 0; i < 4; i += 2) {
+          uint32_t bh[2][2], bl[2][2];         // [column pair][row]
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        uint32_t bh[2][2][2], bl[2][2][2];     // [column pair][row half]
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            split3(e[q][0][i + u], bh[u][q][0], bl[u][q][0]);
-            split3(e[q][1][i + u], bh[u][q][1], bl[u][q][1]);
+          for (int u = 0; u < 2; ++u) {
+            split3(e[0][i + u], bh[u][0], bl[u][0]);
+            split3(e[1][i + u], bh[u][1], bl[u][1]);
           }
-        float c[2][2][4];
-        weight_products(c, zh, zl, bh, bl);
+          float c[2][2][4];
+          weight_products(c, zh, zl, bh, bl);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[m][4 * j + i + u][k] += c[u][m][k];
+              for (int k = 0; k < 4; ++k) acc[m][4 * j + i + u][k] += c[u][m][k];
+        }
       }
     }
     __syncwarp();                            // this stage may be overwritten
   }
+  int tt = t, gg = g;                        // the places below are worked out here, not carried through the loop
+  asm volatile("" : "+r"(tt), "+r"(gg));
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int nn = 16 * m + g + 8 * (k >> 1);
+      const int nn = 16 * m + gg + 8 * (k >> 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = position_column(8 * (i >> 2) + 2 * t + (k & 1), i & 3);
+        const int c = position_column(8 * (i >> 2) + 2 * tt + (k & 1), i & 3);
         G[c < 63 ? nn * 63 + c : O_B1 + nn] = acc[m][i][k];
       }
     }
@@ -661,94 +641,81 @@ __device__ __forceinline__ void backward_w2(const CellsBackwardArgs& P, CellsBac
     BackwardTile& T = S.tile[warp][stage];
     if (lane < CB_ROWS && row0 + lane < cell_end) unit3(&T.v[3 * lane]);
     __syncwarp();
-    float h2[2][4][2], gc[2][2];
-    float4 gr[2][2];
+#pragma unroll 1
+    for (int q = 0; q < CB_ROWS; q += 8) {
+      asm volatile("" ::: "memory");         // the weights' fragments are read anew, not held in registers
+      const int r = q + 2 * t;               // this lane's rows r, r + 1
+      float h2[4][2];
+      uint32_t zh[2][4], zl[2][4];
+      {
+        const float4 g0 = T.d_raw[r], g1 = T.d_raw[r + 1];
+        // g2 as operand A: features g + 8 j of the two rows
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+        for (int j = 0; j < 4; ++j) {
+          const float4 w = S.wh[warp][8 * j + g];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            h2[j][i] = T.hidden[r + i][32 + 8 * j + g];
+            const float z = h2[j][i] > 0.0f ? head_grad(w, i ? g1 : g0) : 0.0f;
+            sb2[j] += z;
+            split3(z, zh[j >> 1][(j & 1) + 2 * i], zl[j >> 1][(j & 1) + 2 * i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) split3(T.hidden[r + i][8 * (j + u) + g], bh[u][i], bl[u][i]);
+        float c[2][2][4];
+        weight_products(c, zh, zl, bh, bl);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[m][j + u][k] += c[u][m][k];
+      }
+      // the heads: rows of A are features of [h2 | gamma(d)], columns of B the
+      // channels. Direction base g < 6 (coordinate g / 2, octave 2 (g % 2)): tile 2
+      // its sine and cosine, tile 3 those of the octave above; rows 6 and 7 hold
+      // u0, u1, u2 and 1.
+      uint32_t gh[2], gl[2];
+      float v[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 8 * q + 2 * t + i;
-        gr[q][i] = T.d_raw[r];
-        gc[q][i] = g < 4 ? reinterpret_cast<const float*>(&T.d_raw[r])[g & 3] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h2[q][j][i] = T.hidden[r][32 + 8 * j + g];
+        split3(g < 4 ? reinterpret_cast<const float*>(&T.d_raw[r + i])[g & 3] : 0.0f, gh[i], gl[i]);
+        const float* e = &T.v[3 * (r + i)];
+        two_octaves(e[g < 6 ? g >> 1 : g - 6], g & 1 ? 4.0f : 1.0f, v[i]);
+        if (g >= 6) {
+          v[i][0] = e[g - 6];
+          v[i][2] = g == 6 ? e[2] : 1.0f;
+          v[i][1] = v[i][3] = 0.0f;
+        }
       }
-    // g2 as operand A: features g + 8 j of rows 8q + 2t + i
-    uint32_t zh[2][2][4], zl[2][2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 w = S.wh[warp][8 * j + g];
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float z = h2[q][j][i] > 0.0f ? head_grad(w, gr[q][i]) : 0.0f;
-          sb2[j] += z;
-          split3(z, zh[q][j >> 1][(j & 1) + 2 * i], zl[q][j >> 1][(j & 1) + 2 * i]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      uint32_t bh[2][2][2], bl[2][2][2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          split3(T.hidden[8 * q + 2 * t][8 * (j + u) + g], bh[u][q][0], bl[u][q][0]);
-          split3(T.hidden[8 * q + 2 * t + 1][8 * (j + u) + g], bh[u][q][1], bl[u][q][1]);
-        }
-      float c[2][2][4];
-      weight_products(c, zh, zl, bh, bl);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int m0 = 0; m0 < 4; m0 += 2) {
+        uint32_t fh[2][4], fl[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][j + u][k] += c[u][m][k];
-    }
-    // the heads: rows of A are features of [h2 | gamma(d)], columns of B the channels
-    uint32_t gh[2][2], gl[2][2];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      split3(gc[q][0], gh[q][0], gl[q][0]);
-      split3(gc[q][1], gh[q][1], gl[q][1]);
-    }
-    // direction base g < 6 (coordinate g / 2, octave 2 (g % 2)): tile 2 its sine and
-    // cosine, tile 3 those of the octave above; rows 6 and 7 hold u0, u1, u2 and 1
-    float v[2][2][4];
+            for (int k = 0; k < 2; ++k)
+              split3(m0 == 0 ? h2[2 * m + k][i] : v[i][2 * m + k], fh[m][2 * i + k], fl[m][2 * i + k]);
+        float c[2][4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+        for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float* e = &T.v[3 * (8 * q + 2 * t + i)];
-        two_octaves(e[g < 6 ? g >> 1 : g - 6], g & 1 ? 4.0f : 1.0f, v[q][i]);
-        if (g >= 6) {
-          v[q][i][0] = e[g - 6];
-          v[q][i][2] = g == 6 ? e[2] : 1.0f;
-          v[q][i][1] = v[q][i][3] = 0.0f;
-        }
+          for (int m = 0; m < 2; ++m) mma_from(p == 0, c[m], p == 0 ? fl[m] : fh[m], p == 1 ? gl : gh);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ah[m0 + m][k] += c[m][k];
       }
-    float c[4][4];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t fh[4][4], fl[4][4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            split3(m < 2 ? h2[q][2 * m + k][i] : v[q][i][2 * (m - 2) + k], fh[m][2 * i + k], fl[m][2 * i + k]);
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          mma_from(q == 0 && p == 0, c[m], p == 0 ? fl[m] : fh[m], p == 1 ? gl[q] : gh[q]);
     }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ah[m][k] += c[m][k];
     __syncwarp();                            // this stage may be overwritten
   }
   G -= O_W2;                                 // by the blob's offsets below
