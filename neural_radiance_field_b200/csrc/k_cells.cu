@@ -111,51 +111,48 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int LEFT>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
-// first[c] = tiles of `rows` rows of the cells before c, first[n_cells] = all of
-// them: each warp scans a run of cells, 32 at a time. Offsets are taken into
-// 0..n and sums kept below 2^30, so no table makes a row index leave its buffer.
-constexpr int TILES_MOST = 1 << 30;
+// The work of a cell in units: one for its start (its weights are staged, its
+// gradient is written) and one per tile of `rows` rows; none without rows.
+// first[c] = units of the cells before c, first[n_cells] = all of them. Each
+// thread sums a run of cells, an odd number of them, which keeps its reads of
+// shared memory clear of the others' banks. Offsets are taken into 0..n and sums
+// kept below 2^30, so no table makes a row index leave its buffer.
+constexpr int UNITS_MOST = 1 << 30;
+__device__ __forceinline__ int units_of(int a, int b, int rows) { return b > a ? (b - a + rows - 1) / rows + 1 : 0; }
 template <int THREADS>
-__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ offset, int64_t n,
-                                            int n_cells, int rows, int* first) {
+__device__ __forceinline__ void unit_prefix(const int32_t* __restrict__ offset, int64_t n, int n_cells, int rows,
+                                            int* first) {
   constexpr int WARPS = THREADS / 32;
   __shared__ int sums[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (n_cells + WARPS * 32 - 1) / (WARPS * 32) * 32, base = warp * per;
-  auto at = [&](int c) { return (int)min(max((int64_t)__ldg(offset + c), (int64_t)0), n); };
-  int carry = 0;
-  for (int i0 = 0; i0 < per && base + i0 < n_cells; i0 += 256) {
-    int v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = base + i0 + 32 * i + lane;
-      v[i] = 32 * i + i0 < per && c < n_cells ? (max(at(c + 1) - at(c), 0) + rows - 1) / rows : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int run = v[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run = min(run + u, TILES_MOST);
-      }
-      const int c = base + i0 + 32 * i + lane;
-      if (32 * i + i0 < per && c < n_cells) first[c] = min(carry + run - v[i], TILES_MOST);
-      carry = min(carry + __shfl_sync(0xffffffffu, run, 31), TILES_MOST);
-    }
-  }
-  if (lane == 0) sums[warp] = carry;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+#pragma unroll 8
+  for (int c = t; c <= n_cells; c += THREADS) first[c] = (int)min(max((int64_t)__ldg(offset + c), (int64_t)0), n);
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w == warp) before = all;
-    all = min(all + sums[w], TILES_MOST);
+  const int per = ((n_cells + THREADS - 1) / THREADS) | 1;
+  const int c0 = min(t * per, n_cells), c1 = min(c0 + per, n_cells);
+  const int last = first[c1];
+  int sum = 0;
+  for (int c = c0; c < c1; ++c) sum = min(sum + units_of(first[c], c + 1 < c1 ? first[c + 1] : last, rows), UNITS_MOST);
+  int run = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run = min(run + u, UNITS_MOST);
   }
-  for (int c = base + lane; c < min(base + per, n_cells); c += 32) first[c] = min(first[c] + before, TILES_MOST);
-  if (threadIdx.x == 0) first[n_cells] = all;
+  if (lane == 31) sums[warp] = run;
+  __syncthreads();                           // and every thread has read the offset behind its run
+  int before = max(run - sum, 0);
+  for (int w = 0; w < warp; ++w) before = min(before + sums[w], UNITS_MOST);
+  for (int c = c0, a = c0 < c1 ? first[c0] : 0; c < c1; ++c) {
+    const int b = c + 1 < c1 ? first[c + 1] : last, u = units_of(a, b, rows);
+    first[c] = before;
+    before = min(before + u, UNITS_MOST);
+    a = b;
+  }
+  if (c1 == n_cells && (c0 < c1 || t == 0)) first[n_cells] = before;
   __syncthreads();
 }
-// the cell of a tile: first[c] <= tile < first[c + 1]
+// the cell of a unit: first[c] <= unit < first[c + 1]
 __device__ __forceinline__ int cell_of(const int* first, int n_cells, int tile) {
   int lo = 0, hi = n_cells;
   while (hi - lo > 1) {
@@ -169,15 +166,19 @@ __device__ __forceinline__ int cell_of(const int* first, int n_cells, int tile) 
 
 constexpr int CF_WARPS = 4, CF_THREADS = CF_WARPS * 32;
 constexpr int CF_ROWS = CF_WARPS * 32;       // rows of a tile, 32 per warp
-constexpr int CF_PER_SM = 4;                 // resident CTAs
-constexpr int CF_WAVES = 3;                  // CTAs of the grid per resident one
+constexpr int CF_PER_SM = 4;
 struct CellsForwardShared {
-  float4 w1[8 * 4 * 32];      // B fragments of W1: [k step][n tile][lane] = (hi, hi, lo, lo)
-  float4 w2[4 * 4 * 32];
+  union {
+    struct {
+      float4 w1[8 * 4 * 32];  // B fragments of W1: [k step][n tile][lane] = (hi, hi, lo, lo)
+      float4 w2[4 * 4 * 32];
+    };
+    int first[EXPERT_MAX + 1];   // units, until this CTA has found where it begins
+  };
+  float raw_w[CELL_NP + 3];   // the next cell's weights as they stand in the blob
   float4 wh[32], wd[27], bh;  // heads (r, g, b, sigma) on h2 and (r, g, b, 0) on gamma(d)
   float b1[32], b2[32];
   float rows[CF_WARPS][2][2][96];             // [warp][stage]: x and d of a warp's 32 rows
-  int first[EXPERT_MAX + 1];
 };
 
 __device__ __forceinline__ float4 b_fragment(float b0, float b1) {
@@ -215,83 +216,103 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
   extern __shared__ __align__(16) uint8_t cells_sm[];
   CellsForwardShared& S = *reinterpret_cast<CellsForwardShared*>(cells_sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  tile_prefix<CF_THREADS>(offset, n, n_cells, CF_ROWS, S.first);
-  const int tiles = S.first[n_cells], per = (tiles + gridDim.x - 1) / gridDim.x;
-  const int end = min(tiles, (int)(blockIdx.x + 1) * per);
-  // A tile's cell and this warp's rows of it, found one tile ahead; its positions
-  // and directions are on their way from then on.
-  struct Tile {
-    int cell;
-    int64_t row0;
-    int rows;                                // 0 or less: none for this warp
-  } now{-1, 0, 0}, next{-1, 0, 0};
-  auto look = [&](int tile, int stage, Tile before) {
-    Tile n_{before.cell, 0, 0};
-    if (tile < end) {
-      if (n_.cell < 0 || tile >= S.first[n_.cell + 1]) n_.cell = cell_of(S.first, n_cells, tile);
-      const int64_t lo = min(max((int64_t)__ldg(offset + n_.cell), (int64_t)0), n);
-      const int64_t hi = min(max((int64_t)__ldg(offset + n_.cell + 1), (int64_t)0), n);
-      n_.row0 = lo + (int64_t)max(tile - S.first[n_.cell], 0) * CF_ROWS + warp * 32;
-      n_.rows = (int)min((int64_t)32, hi - n_.row0);
-      const int have = max(n_.rows, 0) * 3;
-      const int64_t at = have > 0 ? n_.row0 * 3 : 0;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const int e = 32 * q + lane;
-        copy_async4(&S.rows[warp][stage][0][e], x + at + (e < have ? e : 0), e < have);
-        copy_async4(&S.rows[warp][stage][1][e], d + at + (e < have ? e : 0), e < have);
+  unit_prefix<CF_THREADS>(offset, n, n_cells, CF_ROWS, S.first);
+  // This CTA's units [unit, end), an equal share. A place in them: a cell, its
+  // first unit and its rows.
+  const int units = S.first[n_cells], per = (units + gridDim.x - 1) / gridDim.x;
+  const int begin = (int)min((int64_t)blockIdx.x * per, (int64_t)units), end = min(units, begin + per);
+  if (begin >= end) return;
+  auto clamped = [&](int c) { return (int)min(max((int64_t)__ldg(offset + c), (int64_t)0), n); };
+  struct Place {
+    int cell, first;                         // -1: past the end
+    int lo, hi;
+  };
+  Place at;
+  at.cell = cell_of(S.first, n_cells, begin);
+  at.first = S.first[at.cell];
+  at.lo = clamped(at.cell);
+  at.hi = clamped(at.cell + 1);
+  __syncthreads();                           // the units' memory now holds weights
+  // the next cell with rows, found 32 at a time
+  auto behind = [&](Place p) {
+    const int start = p.first + units_of(p.lo, p.hi, CF_ROWS);
+    for (int c0 = p.cell + 1; c0 < n_cells; c0 += 32) {
+      const int c = c0 + lane, lo = c < n_cells ? clamped(c) : 0, hi = c < n_cells ? clamped(c + 1) : 0;
+      const unsigned some = __ballot_sync(0xffffffffu, hi > lo);
+      if (some) {
+        const int l = __ffs(some) - 1;
+        return Place{c0 + l, start, __shfl_sync(0xffffffffu, lo, l), __shfl_sync(0xffffffffu, hi, l)};
       }
     }
-    copy_commit();
-    return n_;
+    return Place{-1, end, 0, 0};
   };
-  int staged = -1, stage = 0;
-  next = look(blockIdx.x * per, 0, now);
-  for (int tile = blockIdx.x * per; tile < end; ++tile, stage ^= 1) {
-    now = next;
-    __syncwarp();                            // the stage's readers, a tile ago, are done
-    next = look(tile + 1, stage ^ 1, now);
-    const int cell = now.cell;
+  // A tile's positions, directions and, where its cell is another than the last
+  // tile's, weights are on their way one tile ahead.
+  auto fetch_rows = [&](const Place& p, int unit, int stage) {
+    const int64_t row0 = p.lo + (int64_t)(unit - p.first - 1) * CF_ROWS + warp * 32;
+    const int have = (int)max(min((int64_t)32, p.hi - row0), (int64_t)0) * 3;
+    const int64_t from = have > 0 ? row0 * 3 : 0;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int e = 32 * q + lane;
+      copy_async4(&S.rows[warp][stage][0][e], x + from + (e < have ? e : 0), e < have);
+      copy_async4(&S.rows[warp][stage][1][e], d + from + (e < have ? e : 0), e < have);
+    }
+  };
+  auto fetch_weights = [&](int cell) {
+    const float* __restrict__ W = cell_w + (int64_t)cell * CELL_NP;
+    for (int q = tid; q < CELL_NP; q += CF_THREADS) copy_async4(&S.raw_w[q], W + q, true);
+  };
+  int unit = max(begin, at.first + 1), staged = -1;
+  fetch_weights(at.cell);
+  fetch_rows(at, unit, 0);
+  copy_commit();
+  for (int stage = 0; unit < end; stage ^= 1) {
+    const int cell = at.cell;
+    copy_wait<0>();                          // this tile's copies
+    __syncwarp();
     if (cell != staged) {
       staged = cell;
-      __syncthreads();                       // the previous cell's weights are no longer read
-      const float* __restrict__ W = cell_w + (int64_t)cell * CELL_NP;
-#pragma unroll
+      __syncthreads();                       // everyone's part of the weights; the last cell's fragments are done with
+      const float* W = S.raw_w;
+#pragma unroll 4
       for (int q = tid; q < 8 * 4 * 32; q += CF_THREADS) {
         const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), s = q >> 7;
         const int base = 4 * (s >> 1) + (l & 3), c1 = position_column(base, 2 * (s & 1) + 1);
-        S.w1[q] = b_fragment(__ldg(W + nn * 63 + position_column(base, 2 * (s & 1))),
-                             c1 < 63 ? __ldg(W + nn * 63 + c1) : 0.0f);
+        S.w1[q] = b_fragment(W[nn * 63 + position_column(base, 2 * (s & 1))], c1 < 63 ? W[nn * 63 + c1] : 0.0f);
       }
 #pragma unroll
       for (int q = tid; q < 4 * 4 * 32; q += CF_THREADS) {
         const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), f = 8 * (q >> 7) + 2 * (l & 3);
-        S.w2[q] = b_fragment(__ldg(W + O_W2 + nn * 32 + f), __ldg(W + O_W2 + nn * 32 + f + 1));
+        S.w2[q] = b_fragment(W[O_W2 + nn * 32 + f], W[O_W2 + nn * 32 + f + 1]);
       }
       if (tid < 32) {
-        S.b1[tid] = __ldg(W + O_B1 + tid);
-        S.b2[tid] = __ldg(W + O_B2 + tid);
+        S.b1[tid] = W[O_B1 + tid];
+        S.b2[tid] = W[O_B2 + tid];
       } else if (tid < 64) {
         const int f = tid - 32;
-        S.wh[f] = make_float4(__ldg(W + O_WC + f), __ldg(W + O_WC + 59 + f), __ldg(W + O_WC + 118 + f),
-                              __ldg(W + O_WS + f));
+        S.wh[f] = make_float4(W[O_WC + f], W[O_WC + 59 + f], W[O_WC + 118 + f], W[O_WS + f]);
       } else if (tid < 91) {
         const int f = tid - 64 + 32;
-        S.wd[tid - 64] = make_float4(__ldg(W + O_WC + f), __ldg(W + O_WC + 59 + f),
-                                     __ldg(W + O_WC + 118 + f), 0.0f);
+        S.wd[tid - 64] = make_float4(W[O_WC + f], W[O_WC + 59 + f], W[O_WC + 118 + f], 0.0f);
       } else if (tid == 91) {
-        S.bh = make_float4(__ldg(W + O_BC), __ldg(W + O_BC + 1), __ldg(W + O_BC + 2), __ldg(W + O_BS));
+        S.bh = make_float4(W[O_BC], W[O_BC + 1], W[O_BC + 2], W[O_BS]);
       }
       __syncthreads();
     }
-    if (now.rows <= 0) continue;
-    copy_wait<1>();                          // this tile's copies; the next tile's may still run
-    __syncwarp();
+    const int64_t row0 = at.lo + (int64_t)(unit - at.first - 1) * CF_ROWS + warp * 32;
+    const int rows = (int)min((int64_t)32, at.hi - row0);
+    if (++unit >= at.first + units_of(at.lo, at.hi, CF_ROWS) && unit < end) {
+      at = behind(at);
+      unit = at.first + 1;
+      if (unit < end) fetch_weights(at.cell);
+    }
+    if (unit < end) fetch_rows(at, unit, stage ^ 1);
+    copy_commit();
+    if (rows <= 0) continue;
     // this warp's 32 rows: lane (g, t) works on rows g + 8 r, r = 0..3
     const float* xs = S.rows[warp][stage][0];
     float* ds = S.rows[warp][stage][1];
-    const int64_t row0 = now.row0;
-    const int rows = now.rows;
     float h[2][4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -443,8 +464,8 @@ struct CellsBackwardShared {
 };
 
 int64_t backward_ctas(int64_t n, int n_cells) {
-  const int64_t tiles = (n + CB_ROWS - 1) / CB_ROWS + (n_cells < n ? n_cells : n);
-  const int64_t ctas = (tiles + CB_B - 1) / CB_B;
+  const int64_t units = (n + CB_ROWS - 1) / CB_ROWS + 2 * (n_cells < n ? n_cells : n);
+  const int64_t ctas = (units + CB_B - 1) / CB_B;
   return ctas < CB_SMS ? ctas : CB_SMS;
 }
 
@@ -761,65 +782,73 @@ __global__ void __launch_bounds__(CB_THREADS, 1) cells_backward_kernel(CellsBack
   extern __shared__ __align__(16) uint8_t cells_sm[];
   CellsBackwardShared& S = *reinterpret_cast<CellsBackwardShared*>(cells_sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  tile_prefix<CB_THREADS>(P.offset, P.n, P.n_cells, CB_ROWS, S.first);
+  unit_prefix<CB_THREADS>(P.offset, P.n, P.n_cells, CB_ROWS, S.first);
   if (blockIdx.x == 0)
     for (int c = tid; c <= P.n_cells; c += CB_THREADS) P.first_out[c] = S.first[c];
   const bool role_a = warp < CB_A;
   const int W = gridDim.x * (role_a ? CB_A : CB_B);
   const int w = role_a ? blockIdx.x * CB_A + warp : blockIdx.x * CB_B + warp - CB_A;
-  const int tiles = S.first[P.n_cells], per = (tiles + W - 1) / W;
-  const int begin = (int)min((int64_t)w * per, (int64_t)tiles), end = min(tiles, begin + per);
-  for (int tile = begin; tile < end;) {
-    const int cell = cell_of(S.first, P.n_cells, tile);
-    const int t0 = S.first[cell], t1 = S.first[cell + 1], stop = min(end, max(t1, tile + 1));
-    const float* __restrict__ W2 = P.cell_w + (int64_t)cell * CELL_NP;
-    __syncwarp();                            // the previous cell's fragments are no longer read
-    S.wh[warp][lane] = make_float4(__ldg(W2 + O_WC + lane), __ldg(W2 + O_WC + 59 + lane),
-                                   __ldg(W2 + O_WC + 118 + lane), __ldg(W2 + O_WS + lane));
-    __syncwarp();
+  const int units = S.first[P.n_cells], per = (units + W - 1) / W;
+  const int begin = (int)min((int64_t)w * per, (int64_t)units), end = min(units, begin + per);
+  for (int unit = begin; unit < end;) {
+    const int cell = cell_of(S.first, P.n_cells, unit);
+    const int u0 = S.first[cell] + 1, u1 = S.first[cell + 1], stop = min(end, max(u1, unit + 1));   // its tiles: [u0, u1)
+    unit = max(unit, u0);
     const int64_t cell_begin = min(max((int64_t)P.offset[cell], (int64_t)0), P.n);
     const int64_t cell_end = min(max((int64_t)P.offset[cell + 1], (int64_t)0), P.n);
-    const int64_t row0 = cell_begin + (int64_t)max(tile - t0, 0) * CB_ROWS;
-    const bool whole = t0 >= begin && t1 <= end;
-    const int64_t slot = (int64_t)w * 2 + (t0 > begin ? 1 : 0);
-    if (row0 < cell_end) {
+    const int64_t row0 = cell_begin + (int64_t)(unit - u0) * CB_ROWS;
+    if (unit < stop && row0 < cell_end) {
+      const float* __restrict__ W2 = P.cell_w + (int64_t)cell * CELL_NP;
+      __syncwarp();                          // the previous cell's fragments are no longer read
+      S.wh[warp][lane] = make_float4(__ldg(W2 + O_WC + lane), __ldg(W2 + O_WC + 59 + lane),
+                                     __ldg(W2 + O_WC + 118 + lane), __ldg(W2 + O_WS + lane));
+      __syncwarp();
+      const bool whole = u0 >= begin && u1 <= end;
+      const int64_t slot = (int64_t)w * 2 + (u0 > begin ? 1 : 0);
       if (role_a)
-        backward_w1(P, S, warp, lane, W2, row0, cell_end, stop - tile,
+        backward_w1(P, S, warp, lane, W2, row0, cell_end, stop - unit,
                     whole ? P.grad + (int64_t)cell * CELL_NP : P.parts_a + slot * CB_NA);
       else
-        backward_w2(P, S, warp, lane, row0, cell_end, stop - tile,
+        backward_w2(P, S, warp, lane, row0, cell_end, stop - unit,
                     whole ? P.grad + (int64_t)cell * CELL_NP + O_W2 : P.parts_b + slot * CB_NB);
     }
-    tile = stop;
+    unit = stop;
   }
 }
 
 // One CTA per cell: nothing where one warp wrote it, zeros where it has no rows,
 // the sum of its parts in warp order where several did; for each role.
+template <int N, int WARPS>
+__device__ __forceinline__ void join_parts(int u0, int u1, int units, int ctas, const float* __restrict__ parts,
+                                           float* __restrict__ out) {
+  const int per = (units + ctas * WARPS - 1) / (ctas * WARPS), w0 = u0 / per, w1 = (u1 - 1) / per;
+  if (w0 == w1) return;
+  constexpr int Q = (N + 255) / 256;
+  const float* p = parts + ((int64_t)w0 * 2 + (u0 > w0 * per ? 1 : 0)) * N + threadIdx.x;
+  float s[Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) s[i] = 256 * i + (int)threadIdx.x < N ? __ldcs(p + 256 * i) : 0.0f;
+#pragma unroll 2
+  for (int w = w0 + 1; w <= w1; ++w) {
+    p = parts + (int64_t)w * 2 * N + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) s[i] += 256 * i + (int)threadIdx.x < N ? __ldcs(p + 256 * i) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+    if (256 * i + (int)threadIdx.x < N) out[256 * i + threadIdx.x] = s[i];
+}
 __global__ void __launch_bounds__(256)
-cells_join_kernel(const int* __restrict__ first, int n_cells, int ctas,
-                  const float* __restrict__ parts_a, const float* __restrict__ parts_b,
-                  float* __restrict__ grad) {
-  const int cell = blockIdx.x, t0 = first[cell], t1 = first[cell + 1], tiles = first[n_cells];
+cells_join_kernel(const int* __restrict__ first, int n_cells, int ctas, const float* __restrict__ parts_a,
+                  const float* __restrict__ parts_b, float* __restrict__ grad) {
+  const int cell = blockIdx.x, u0 = first[cell] + 1, u1 = first[cell + 1], units = first[n_cells];
   float* __restrict__ G = grad + (int64_t)cell * CELL_NP;
-  if (t0 >= t1) {
+  if (u0 >= u1) {
     for (int q = threadIdx.x; q < CELL_NP; q += 256) G[q] = 0.0f;
     return;
   }
-#pragma unroll
-  for (int role = 0; role < 2; ++role) {
-    const int W = ctas * (role ? CB_B : CB_A), per = (tiles + W - 1) / W;
-    const int w0 = t0 / per, w1 = (t1 - 1) / per, N = role ? CB_NB : CB_NA;
-    if (w0 == w1) continue;
-    const float* __restrict__ parts = role ? parts_b : parts_a;
-    float* __restrict__ out = role ? G + O_W2 : G;
-    for (int q = threadIdx.x; q < N; q += 256) {
-      float s = parts[((int64_t)w0 * 2 + (t0 > w0 * per ? 1 : 0)) * N + q];
-#pragma unroll 8
-      for (int w = w0 + 1; w <= w1; ++w) s += parts[(int64_t)w * 2 * N + q];
-      out[q] = s;
-    }
-  }
+  join_parts<CB_NA, CB_A>(u0, u1, units, ctas, parts_a, G);
+  join_parts<CB_NB, CB_B>(u0, u1, units, ctas, parts_b, G + O_W2);
 }
 
 }  // namespace
@@ -830,8 +859,8 @@ cudaError_t launch_cells_forward(const float* x, const float* d, int64_t n, cons
   const size_t sm = sizeof(CellsForwardShared);
   cudaError_t e = cudaFuncSetAttribute(cells_forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (n + CF_ROWS - 1) / CF_ROWS + (n_cells < n ? n_cells : n);
-  constexpr int64_t most = 148 * CF_PER_SM * CF_WAVES;
+  const int64_t tiles = (n + CF_ROWS - 1) / CF_ROWS + 2 * (n_cells < n ? n_cells : n);   // units at most
+  constexpr int64_t most = 148 * CF_PER_SM;
   const unsigned grid = (unsigned)(tiles < most ? tiles : most);
   cells_forward_kernel<<<grid, CF_THREADS, sm, st>>>(x, d, n, offset, n_cells, cell_w, raw, hidden);
   return cudaGetLastError();
