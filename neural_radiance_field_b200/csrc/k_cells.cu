@@ -188,6 +188,9 @@ __device__ __forceinline__ float4 b_fragment(float b0, float b1) {
   return make_float4(__uint_as_float(h0), __uint_as_float(h1), __uint_as_float(l0), __uint_as_float(l1));
 }
 
+// The feature of column n of output tile j. Lane t, whose columns are 2t and
+// 2t + 1 of the four tiles, has features 8t .. 8t + 7: a run that it stores at once.
+__device__ __forceinline__ int out_feature(int j, int n) { return 8 * (n >> 1) + 2 * j + (n & 1); }
 // One k step of a layer: 32 rows (two fragments) x 32 outputs (four). The three
 // products of an accumulator are eight instructions apart.
 __device__ __forceinline__ void layer_step(float (&c)[2][4][4], const uint32_t (&ah)[2][4],
@@ -206,6 +209,19 @@ __device__ __forceinline__ void layer_step(float (&c)[2][4][4], const uint32_t (
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         mma_tf32(c[m][j], p == 0 ? al[m] : ah[m], p == 1 ? bl[j][0] : bh[j][0], p == 1 ? bl[j][1] : bh[j][1]);
+}
+
+// a hidden layer of 32 rows (h0 its first row's): lane (g, t) has features 8t .. 8t + 7
+// of rows g + 8 r
+__device__ __forceinline__ void store_hidden(float* __restrict__ h0, const float (&h)[2][4][4], int g, int t, int rows) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (g + 8 * r < rows) {
+      float4* out = reinterpret_cast<float4*>(h0 + (g + 8 * r) * 64 + 8 * t);
+      const int m = r >> 1, i = 2 * (r & 1);
+      out[0] = make_float4(h[m][0][i], h[m][0][i + 1], h[m][1][i], h[m][1][i + 1]);
+      out[1] = make_float4(h[m][2][i], h[m][2][i + 1], h[m][3][i], h[m][3][i + 1]);
+    }
 }
 
 __global__ void __launch_bounds__(CF_THREADS, CF_PER_SM)
@@ -277,13 +293,13 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
       const float* W = S.raw_w;
 #pragma unroll 4
       for (int q = tid; q < 8 * 4 * 32; q += CF_THREADS) {
-        const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), s = q >> 7;
+        const int l = q & 31, nn = out_feature((q >> 5) & 3, l >> 2), s = q >> 7;
         const int base = 4 * (s >> 1) + (l & 3), c1 = position_column(base, 2 * (s & 1) + 1);
         S.w1[q] = b_fragment(W[nn * 63 + position_column(base, 2 * (s & 1))], c1 < 63 ? W[nn * 63 + c1] : 0.0f);
       }
 #pragma unroll
       for (int q = tid; q < 4 * 4 * 32; q += CF_THREADS) {
-        const int l = q & 31, nn = 8 * ((q >> 5) & 3) + (l >> 2), f = 8 * (q >> 7) + 2 * (l & 3);
+        const int l = q & 31, nn = out_feature((q >> 5) & 3, l >> 2), f = 8 * (l & 3) + 2 * (q >> 7);
         S.w2[q] = b_fragment(W[O_W2 + nn * 32 + f], W[O_W2 + nn * 32 + f + 1]);
       }
       if (tid < 32) {
@@ -316,7 +332,7 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
     float h[2][4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 b = *reinterpret_cast<const float2*>(&S.b1[8 * j + 2 * t]);
+      const float2 b = *reinterpret_cast<const float2*>(&S.b1[8 * t + 2 * j]);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         h[m][j][0] = h[m][j][2] = b.x;
@@ -343,23 +359,17 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
     float h2[2][4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 b = *reinterpret_cast<const float2*>(&S.b2[8 * j + 2 * t]);
+      const float2 b = *reinterpret_cast<const float2*>(&S.b2[8 * t + 2 * j]);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         h2[m][j][0] = h2[m][j][2] = b.x;
         h2[m][j][1] = h2[m][j][3] = b.y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[m][j][i] = fmaxf(h[m][j][i], 0.0f);
-        if (hidden) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (g + 8 * (2 * m + i) < rows)
-              *reinterpret_cast<float2*>(hidden + (row0 + g + 8 * (2 * m + i)) * 64 + 8 * j + 2 * t) =
-                  make_float2(h[m][j][2 * i], h[m][j][2 * i + 1]);
-        }
       }
     }
-    // h1's fragment (row, columns 8s + 2t, 8s + 2t + 1) is the operand of k step
+    if (hidden) store_hidden(hidden + row0 * 64, h, g, t, rows);
+    // h1's fragment (row, features 8t + 2s, 8t + 2s + 1) is the operand of k step
     // s with its columns t, t + 4 standing for those two features
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -370,17 +380,22 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
         for (int i = 0; i < 4; ++i) split3(h[m][s][i], ah[m][(i & 1) * 2 + (i >> 1)], al[m][(i & 1) * 2 + (i >> 1)]);
       layer_step(h2, ah, al, &S.w2[s * 128 + lane]);
     }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h2[m][j][i] = fmaxf(h2[m][j][i], 0.0f);
+    if (hidden) store_hidden(hidden + row0 * 64 + 32, h2, g, t, rows);
     // the heads on the FMA pipe, which the tensor products leave idle: each lane
     // its eight features of h2 and its share of gamma(d), for four rows
     float o[4][4] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float4 w0 = S.wh[8 * j + 2 * t], w1 = S.wh[8 * j + 2 * t + 1];
+      const float4 w0 = S.wh[8 * t + 2 * j], w1 = S.wh[8 * t + 2 * j + 1];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float a = fmaxf(h2[r >> 1][j][2 * (r & 1)], 0.0f), b = fmaxf(h2[r >> 1][j][2 * (r & 1) + 1], 0.0f);
-        if (hidden && g + 8 * r < rows)
-          *reinterpret_cast<float2*>(hidden + (row0 + g + 8 * r) * 64 + 32 + 8 * j + 2 * t) = make_float2(a, b);
+        const float a = h2[r >> 1][j][2 * (r & 1)], b = h2[r >> 1][j][2 * (r & 1) + 1];
         o[r][0] = fmaf(w0.x, a, fmaf(w1.x, b, o[r][0]));
         o[r][1] = fmaf(w0.y, a, fmaf(w1.y, b, o[r][1]));
         o[r][2] = fmaf(w0.z, a, fmaf(w1.z, b, o[r][2]));
@@ -391,25 +406,32 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
     // coordinate t and its four octaves
     unit3(ds + 3 * lane);
     __syncwarp();
+    const int tc = min(t, 2);
+    const float on = t < 3 ? 1.0f : 0.0f;    // lane 3 adds nothing
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float ut = ds[3 * (g + 8 * r) + min(t, 2)];
-      float v[8];
-      two_octaves(ut, 1.0f, v);
-      two_octaves(ut, 4.0f, v + 4);
-      if (t < 3) {
-        const float4 wu = S.wd[t];
-        o[r][0] = fmaf(wu.x, ut, o[r][0]);
-        o[r][1] = fmaf(wu.y, ut, o[r][1]);
-        o[r][2] = fmaf(wu.z, ut, o[r][2]);
+    for (int half = 0; half < 2; ++half) {   // octaves 0, 1 and 2, 3
+      float v[4][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 a = S.wd[3 + 12 * (i & 1) + 4 * t + (i >> 1)];
-          o[r][0] = fmaf(a.x, v[i], o[r][0]);
-          o[r][1] = fmaf(a.y, v[i], o[r][1]);
-          o[r][2] = fmaf(a.z, v[i], o[r][2]);
+      for (int r = 0; r < 4; ++r) two_octaves(ds[3 * (g + 8 * r) + tc], half ? 4.0f : 1.0f, v[r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 a = S.wd[3 + 12 * (i & 1) + 4 * tc + 2 * half + (i >> 1)];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = v[r][i] * on;
+          o[r][0] = fmaf(a.x, e, o[r][0]);
+          o[r][1] = fmaf(a.y, e, o[r][1]);
+          o[r][2] = fmaf(a.z, e, o[r][2]);
         }
       }
+    }
+    const float4 wu = S.wd[tc];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float ut = ds[3 * (g + 8 * r) + tc] * on;
+      o[r][0] = fmaf(wu.x, ut, o[r][0]);
+      o[r][1] = fmaf(wu.y, ut, o[r][1]);
+      o[r][2] = fmaf(wu.z, ut, o[r][2]);
     }
     // sum over the four lanes of a row; lane t keeps row g + 8 t
     float4 v;
