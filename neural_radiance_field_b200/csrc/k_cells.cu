@@ -464,7 +464,7 @@ cells_forward_kernel(const float* __restrict__ x, const float* __restrict__ d, i
 // with the number of additions and all in one direction (2e-6 of the gradient
 // at 370 rows a cell); so a tile's products go to a fresh accumulator, which is
 // added to the cell's by a rounded addition.
-constexpr int CB_A = 6, CB_B = 6;             // warps of each role in a CTA (measured: 8 and 4 297 us, 7 and 5 260, 6 and 6 241)
+constexpr int CB_A = 7, CB_B = 5;             // warps of each role in a CTA (8 and 4: 210 us, 6 and 6: 206, 7 and 5: 196)
 constexpr int CB_THREADS = (CB_A + CB_B) * 32;
 constexpr int CB_ROWS = 16;
 constexpr int CB_SMS = 148;

@@ -207,10 +207,54 @@ __device__ __forceinline__ float2 cluster_join(float2 v, float c, float2* stat, 
 }
 
 constexpr float kLog2e = 1.44269504f;
-// -inf, once or twice in a word
-template <typename T> constexpr uint32_t kNegInf = 0xff800000u;
-template <> constexpr uint32_t kNegInf<__nv_bfloat16> = 0xff80ff80u;
-template <> constexpr uint32_t kNegInf<__half> = 0xfc00fc00u;
+
+// The passes over one vector, two elements an instruction where there is one.
+// Maximum: into four words of elements.
+template <typename T, typename V>
+__device__ __forceinline__ void pass_max(const V& v, uint32_t* top) {
+#pragma unroll
+  for (int w = 0; w < V::W; ++w) top[w & 3] = word_max<T>(top[w & 3], v.words[w]);
+}
+template <typename T>
+__device__ __forceinline__ float whole_max(const uint32_t* top, float one) {
+  const uint32_t w = word_max<T>(word_max<T>(top[0], top[1]), word_max<T>(top[2], top[3]));
+  return max_nan(one, max_nan(word_elem<T>(w, 0), word_elem<T>(w, 1)));   // an fp32 word has one element, twice
+}
+// 2^((v - m) c) of elements 2i and 2i + 1; less: -m twice, c2: c twice
+template <typename V>
+__device__ __forceinline__ void pair_exp(const V& v, int i, F2 less, F2 c2, float& a, float& b) {
+  ((v.pair(i) + less) * c2).split(a, b);
+  a = exp2_fast(a);
+  b = exp2_fast(b);
+}
+template <typename V>
+__device__ __forceinline__ void pass_sum(const V& v, F2 less, F2 c2, F2* z) {
+#pragma unroll
+  for (int i = 0; i < V::N / 2; ++i) {
+    float a, b;
+    pair_exp(v, i, less, c2, a, b);
+    z[i & 1] = z[i & 1] + F2::of(a, b);
+  }
+}
+__device__ __forceinline__ float whole_sum(const F2* z) {
+  float a, b;
+  (z[0] + z[1]).split(a, b);
+  return a + b;
+}
+// The vector's gradient, aiz 2^((v - m) c), packed.
+template <typename V>
+__device__ __forceinline__ V pass_grad(const V& v, F2 less, F2 c2, F2 aiz2) {
+  float f[V::N];
+#pragma unroll
+  for (int i = 0; i < V::N / 2; ++i) {
+    float a, b;
+    pair_exp(v, i, less, c2, a, b);
+    (F2::of(a, b) * aiz2).split(f[2 * i], f[2 * i + 1]);
+  }
+  V o;
+  o.pack(f);
+  return o;
+}
 
 // The part of a row that CTA `rank` of `C` holds: vectors [v0, v1) of the row,
 // and single elements (the first CTA those before the vectors, the last those after).
@@ -245,6 +289,7 @@ distill_rows_kernel(DistillArgs A) {
   float* probs = probs_s[warp];
   int32_t* ids = ids_s[warp];
   const float c = kLog2e / A.temperature;
+  const F2 c2 = F2::of(c, c);
   for (int64_t i = (int64_t)blockIdx.x * 8 + warp; i < A.n; i += (int64_t)gridDim.x * 8) {
     const T* s = (const T*)A.student + i * A.classes;
     T* g = A.grad ? (T*)A.grad + i * A.classes : nullptr;
@@ -263,27 +308,23 @@ distill_rows_kernel(DistillArgs A) {
     teacher_solve(A, i, R, probs, ids);
     // The passes go over groups of four vectors, each behind a condition that the
     // warp shares: unused groups are skipped, and a row of 16-bit elements is never
-    // unpacked as a whole, which would not fit the registers. Four maxima and four
-    // sums run side by side: one chain would wait for itself.
+    // unpacked as a whole, which would not fit the registers.
     const int used = (P.v1 + 31) / 32;
-    float mp[4] = {one, one, one, one};
+    uint32_t top[4] = {kNegInf<T>, kNegInf<T>, kNegInf<T>, kNegInf<T>};
 #pragma unroll
     for (int q0 = 0; q0 < NV; q0 += 4)
       if (q0 < used)
 #pragma unroll
-        for (int q = q0; q < q0 + 4 && q < NV; ++q)
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], v[q].get(e));
-    const float m = warp_max(max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3])));
-    float zp[4] = {exp2_fast((one - m) * c), 0.0f, 0.0f, 0.0f};
+        for (int q = q0; q < q0 + 4 && q < NV; ++q) pass_max<T>(v[q], top);
+    const float m = warp_max(whole_max<T>(top, one));
+    const F2 less = F2::of(-m, -m);
+    F2 zp[2] = {F2::of(exp2_fast((one - m) * c), 0.0f), F2::of(0.0f, 0.0f)};
 #pragma unroll
     for (int q0 = 0; q0 < NV; q0 += 4)
       if (q0 < used)
 #pragma unroll
-        for (int q = q0; q < q0 + 4 && q < NV; ++q)
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((v[q].get(e) - m) * c);
-    const float z = warp_sum((zp[0] + zp[1]) + (zp[2] + zp[3]));
+        for (int q = q0; q < q0 + 4 && q < NV; ++q) pass_sum(v[q], less, c2, zp);
+    const float z = warp_sum(whole_sum(zp));
     const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f), aiz = a / z;
     if (g) {
       T* gv = g + P.head;
@@ -292,11 +333,7 @@ distill_rows_kernel(DistillArgs A) {
         if (R.some && q0 < used) {
 #pragma unroll
           for (int q = q0; q < q0 + 4 && q < NV; ++q) {
-            float f[V::N];
-#pragma unroll
-            for (int e = 0; e < V::N; ++e) f[e] = exp2_fast((v[q].get(e) - m) * c) * aiz;
-            V o;
-            o.pack(f);
+            const V o = pass_grad(v[q], less, c2, F2::of(aiz, aiz));
             if (q * 32 < nv) o.store(gv, r + q * 32);
           }
         } else if (q0 < used) {
@@ -340,6 +377,7 @@ distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
   const int t = threadIdx.x, rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank();
   const bool teacher = t >= DS_M;
   const float c = kLog2e / A.temperature;
+  const F2 c2 = F2::of(c, c);
   const int64_t step = gridDim.x / C;
   int64_t i = blockIdx.x / C;
   if (C > 1) cg::this_cluster().sync();      // every CTA runs before one writes to another
@@ -389,37 +427,28 @@ distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
       const int nv = P.v1 - P.v0;
       const float a = A.temperature * (A.scale ? __ldg(A.scale + i) : 1.0f);
       copy_wait<1>();                        // this row's copies; the next row's may still run
-      float mp[4] = {one, one, one, one};
+      uint32_t mp[4] = {kNegInf<T>, kNegInf<T>, kNegInf<T>, kNegInf<T>};
 #pragma unroll 2
-      for (int q = t; q < nv; q += DS_M) {
-        const V x = V::of(v[q]);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) mp[e & 3] = max_nan(mp[e & 3], x.get(e));
-      }
-      const float top = max_nan(max_nan(mp[0], mp[1]), max_nan(mp[2], mp[3]));
+      for (int q = t; q < nv; q += DS_M) pass_max<T>(V::of(v[q]), mp);
+      const float top = whole_max<T>(mp, one);
       const float shift = top == -INFINITY ? 0.0f : top;
-      float zp[4] = {exp2_fast((one - shift) * c), 0.0f, 0.0f, 0.0f};
+      F2 zp[2] = {F2::of(exp2_fast((one - shift) * c), 0.0f), F2::of(0.0f, 0.0f)};
 #pragma unroll 2
-      for (int q = t; q < nv; q += DS_M) {
-        const V x = V::of(v[q]);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) zp[e & 3] += exp2_fast((x.get(e) - shift) * c);
-      }
-      float2 all = cta_join<DS_T>(make_float2(top, (zp[0] + zp[1]) + (zp[2] + zp[3])), c, red[turn]);
+      for (int q = t; q < nv; q += DS_M) pass_sum(V::of(v[q]), F2::of(-shift, -shift), c2, zp);
+      float2 all = cta_join<DS_T>(make_float2(top, whole_sum(zp)), c, red[turn]);
       if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
       const float m = all.x, aiz = a / all.y;
       const bool some = some_s[turn];
       if (g) {
         T* gv = g + P.head;
+        if (some) {
 #pragma unroll 2
-        for (int q = t; q < nv; q += DS_M) {
-          const V x = V::of(v[q]);
-          float f[V::N];
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) f[e] = some ? exp2_fast((x.get(e) - m) * c) * aiz : 0.0f;
+          for (int q = t; q < nv; q += DS_M)
+            pass_grad(V::of(v[q]), F2::of(-m, -m), c2, F2::of(aiz, aiz)).store(gv, P.v0 + q);
+        } else {
           V o;
-          o.pack(f);
-          o.store(gv, P.v0 + q);
+          o.fill(0);
+          for (int q = t; q < nv; q += DS_M) o.store(gv, P.v0 + q);
         }
         if (P.has) g[P.single] = elem_from_f<T>(some ? exp2_fast((one - m) * c) * aiz : 0.0f);
         asm volatile("bar.arrive 1, %0;" ::"n"(DS_T) : "memory");

@@ -41,6 +41,49 @@ template <> __device__ __forceinline__ uint32_t word_from_f<__half>(float lo, fl
   return w;
 }
 
+// the larger of each element of two words; a NaN stays
+template <typename T> __device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t word_max<float>(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <> __device__ __forceinline__ uint32_t word_max<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <> __device__ __forceinline__ uint32_t word_max<__half>(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+// -inf in every element of a word
+template <typename T> constexpr uint32_t kNegInf = 0xff800000u;
+template <> constexpr uint32_t kNegInf<__nv_bfloat16> = 0xff80ff80u;
+template <> constexpr uint32_t kNegInf<__half> = 0xfc00fc00u;
+
+// Two fp32 values in one register pair: one instruction for both.
+struct F2 {
+  uint64_t v;
+  static __device__ __forceinline__ F2 of(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+  }
+  __device__ __forceinline__ void split(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // N elements of T in one load or store of 16, 4 or 2 bytes, held as 32-bit words
 // (kept as single 16-bit elements they would take a register each).
 template <typename T, int BYTES>
@@ -77,6 +120,8 @@ struct Vec {
     for (int i = 0; i < W; ++i) words[i] = w;
   }
   __device__ __forceinline__ float get(int i) const { return word_elem<T>(words[i / PER], i % PER); }
+  // elements 2i and 2i + 1
+  __device__ __forceinline__ F2 pair(int i) const { return F2::of(get(2 * i), get(2 * i + 1)); }
   __device__ __forceinline__ void pack(const float* v) {
 #pragma unroll
     for (int i = 0; i < W; ++i) words[i] = word_from_f<T>(v[PER * i], N > 1 ? v[(PER * i + 1) % N] : 0.0f);
