@@ -125,20 +125,25 @@ def nerf_test_sh(d, out, stream=None):
     _capi.check(_capi.lib().nerf_test_sh(_ptr(d), d.shape[0], _ptr(out), _stream(stream)))
 
 
-def _device():
-    """The current device; before CUDA is up no tensor can be on one."""
+def _current(name, t):
+    """The device of an operator's first tensor, which has to be the current one (the C
+    ABI works on that)."""
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on cuda:{dev}, which is not the current device")
+    return dev
 
 
 def _arg(name, t, dtype, shape, dev):
-    """Address of a tensor argument: contiguous, of the given type and shape, on the
-    current device `dev` (the C ABI works on that one)."""
+    """Address of a tensor argument: contiguous, of the given type and shape, on device `dev`."""
     try:
         if t.dtype is not dtype or t.shape != shape:
             raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
         if t.get_device() != dev:
-            raise ValueError(f"{name}: expected a CUDA tensor on the current device ({dev}), got one on {t.device}")
+            raise ValueError(f"{name}: expected a CUDA tensor on the current device (cuda:{dev}), got one on {t.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous tensor")
         return t.data_ptr()
@@ -202,7 +207,7 @@ def nerf_expert_sort(ids, n_experts, out_offset, out_order, out_pos, workspace, 
     or None; workspace: any tensor of at least nerf_expert_sort_workspace bytes."""
     import torch
     n, k = _shape2("ids", ids)
-    i32, dev, e = torch.int32, _device(), int(n_experts)
+    i32, dev, e = torch.int32, _current("ids", ids), int(n_experts)
     _call("nerf_expert_sort", _arg("ids", ids, i32, (n, k), dev), n, k, e,
           _arg("out_offset", out_offset, i32, (e + 1,), dev), _opt("out_order", out_order, i32, (n * k,), dev),
           _arg("out_pos", out_pos, i32, (n, k), dev), *_work(workspace, dev), stream=stream, dev=dev)
@@ -212,7 +217,7 @@ def nerf_expert_dispatch(x, pos, rows, weights=None, stream=None):
     """rows[pos[i, j]] = weights[i, j] * x[i]; x [n, width], pos [n, k], rows [n * k, width]."""
     import torch
     (n, c), k = _shape2("x", x), _shape2("pos", pos)[1]
-    (t, code), dev = _rows_dtype("x", x), _device()
+    (t, code), dev = _rows_dtype("x", x), _current("x", x)
     _call("nerf_expert_dispatch", _arg("x", x, t, (n, c), dev), code, n, c,
           _arg("pos", pos, torch.int32, (n, k), dev), k,
           _opt("weights", weights, torch.float32, (n, k), dev), _arg("rows", rows, t, (n * k, c), dev),
@@ -223,7 +228,7 @@ def nerf_expert_dispatch_backward(d_rows, x, pos, d_x, weights=None, d_weights=N
     """d_x and d_weights of nerf_expert_dispatch (either may be None); see the header."""
     import torch
     c, (n, k) = _shape2("d_rows", d_rows)[1], _shape2("pos", pos)
-    (t, code), dev, f32 = _rows_dtype("d_rows", d_rows), _device(), torch.float32
+    (t, code), dev, f32 = _rows_dtype("d_rows", d_rows), _current("d_rows", d_rows), torch.float32
     _call("nerf_expert_dispatch_backward", _arg("d_rows", d_rows, t, (n * k, c), dev),
           _opt("x", x, t, (n, c), dev), code, n, c, _arg("pos", pos, torch.int32, (n, k), dev), k,
           _opt("weights", weights, f32, (n, k), dev), _opt("d_x", d_x, t, (n, c), dev),
@@ -234,7 +239,7 @@ def nerf_expert_combine(rows, pos, out, weights=None, stream=None):
     """out[i] = sum_j weights[i, j] * rows[pos[i, j]]; rows [n * k, width], out [n, width]."""
     import torch
     c, (n, k) = _shape2("rows", rows)[1], _shape2("pos", pos)
-    (t, code), dev = _rows_dtype("rows", rows), _device()
+    (t, code), dev = _rows_dtype("rows", rows), _current("rows", rows)
     _call("nerf_expert_combine", _arg("rows", rows, t, (n * k, c), dev), code, n, c,
           _arg("pos", pos, torch.int32, (n, k), dev), k,
           _opt("weights", weights, torch.float32, (n, k), dev), _arg("out", out, t, (n, c), dev),
@@ -246,7 +251,7 @@ def nerf_expert_combine_backward(d_out, rows, pos, d_rows, weights=None, d_weigh
     """d_rows and d_weights of nerf_expert_combine (either may be None); see the header."""
     import torch
     (n, c), k = _shape2("d_out", d_out), _shape2("pos", pos)[1]
-    (t, code), dev, f32 = _rows_dtype("d_out", d_out), _device(), torch.float32
+    (t, code), dev, f32 = _rows_dtype("d_out", d_out), _current("d_out", d_out), torch.float32
     _call("nerf_expert_combine_backward", _arg("d_out", d_out, t, (n, c), dev),
           _opt("rows", rows, t, (n * k, c), dev), code, n, c, _arg("pos", pos, torch.int32, (n, k), dev), k,
           _opt("weights", weights, f32, (n, k), dev), _opt("d_rows", d_rows, t, (n * k, c), dev),
@@ -259,7 +264,7 @@ def nerf_distill_topk(student, teacher_logits, teacher_ids, temperature, out_los
     against a teacher's kept logits and ids [n, k]; see the header."""
     import torch
     (n, e), k = _shape2("student", student), _shape2("teacher_ids", teacher_ids)[1]
-    (t, code), dev, f32 = _rows_dtype("student", student), _device(), torch.float32
+    (t, code), dev, f32 = _rows_dtype("student", student), _current("student", student), torch.float32
     _call("nerf_distill_topk", _arg("student", student, t, (n, e), dev), code, n, e,
           _arg("teacher_logits", teacher_logits, f32, (n, k), dev),
           _arg("teacher_ids", teacher_ids, torch.int32, (n, k), dev), k, float(temperature),
@@ -271,7 +276,7 @@ def nerf_cells_forward(x, d, offset, cell_w, out_raw, out_hidden=None, stream=No
     """Per-cell networks on rows sorted by cell: out_raw [n, 4], out_hidden [n, 64] or None."""
     import torch
     n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
-    f32, dev = torch.float32, _device()
+    f32, dev = torch.float32, _current("x", x)
     _call("nerf_cells_forward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
           _arg("offset", offset, torch.int32, (e + 1,), dev), e,
           _arg("cell_w", cell_w, f32, (e, 3317), dev), _arg("out_raw", out_raw, f32, (n, 4), dev),
@@ -289,7 +294,7 @@ def nerf_cells_backward(x, d, offset, cell_w, hidden, d_raw, grad_cell_w, worksp
     """Weight gradient of nerf_cells_forward (overwritten), from its hidden layers."""
     import torch
     n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
-    f32, dev = torch.float32, _device()
+    f32, dev = torch.float32, _current("x", x)
     _call("nerf_cells_backward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
           _arg("offset", offset, torch.int32, (e + 1,), dev), e,
           _arg("cell_w", cell_w, f32, (e, 3317), dev), _arg("hidden", hidden, f32, (n, 64), dev),
