@@ -86,6 +86,24 @@ def test_sort(torch, n, k, e, kind):
     assert torch.equal(off, off2) and torch.equal(pos, pos2)
 
 
+@pytest.mark.parametrize("n,k,e", [(1300001, 8, 4096), (3700000, 8, 7), (2500, 2, 1025)])
+def test_sort_of_many_tiles(torch, n, k, e):
+    """Chunks of several tiles, three CTAs to an SM, and a chunk that ends inside a tile, against torch's sort."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    ids = (e * torch.rand(n, k, generator=g, device="cuda") ** 3).int().clamp_(max=e - 1)
+    ids[torch.rand(n, k, generator=g, device="cuda") < 0.05] = -1
+    off, order, pos = _sorted(torch, ids, e)
+    key = torch.where(ids < 0, e, ids).reshape(-1)
+    by, ref = torch.sort(key, stable=True)
+    m = int((by < e).sum())
+    assert torch.equal(order[:m].long(), ref[:m]) and (order[m:] == -7).all()
+    assert torch.equal(off.long(), torch.searchsorted(by, torch.arange(e + 1, device="cuda", dtype=by.dtype)))
+    place = torch.empty_like(ref)
+    place[ref] = torch.arange(n * k, device="cuda")
+    assert torch.equal(pos.reshape(-1).long(), torch.where(key < e, place, -1))
+
+
 def test_sort_agrees_with_the_cell_router(torch):
     """One cell per point: the same counts and cells as nerf_test_route_cells."""
     import neural_radiance_field_b200 as nb
@@ -425,6 +443,22 @@ def test_cells(torch, name):
     assert torch.equal(grad, again)
 
 
+def test_cells_far_positions(torch):
+    """Positions far outside the grid: the angles' quadrants are still exact."""
+    import neural_radiance_field_b200 as nb
+    x = np.array([[100.25, -2999.7, 0.1], [2.0 ** 23, 3.0, -2.0 ** 24], [-1023.5, 511.75, 4095.0625], [0.0, -0.0, 1e-30]], np.float32)
+    d = np.array([[1, 2, 3], [0, 0, -2], [1e-20, 1e-20, 0], [1e18, 0, 1e18]], np.float32)
+    w = kilonerf_weights(3, n_cells=1)
+    off = np.array([0, 4], np.int32)
+    raw, hid = torch.empty(4, 4, device="cuda"), torch.empty(4, 64, device="cuda")
+    nb.nerf_cells_forward(_cuda(torch, x), _cuda(torch, d), _cuda(torch, off), _cuda(torch, w), raw, hid)
+    r_raw, r_hid = E.cells_forward(x, d, off, w)
+    # the layers' bound of test_cells, over the largest input of a row; and the oracle's own angle, pi v in fp64:
+    # 2^-53 * pi * 512 * 2^24 = 3e-6 at most
+    e = 64 * (4.5 * 2.0 ** -23 + 3e-6) + (C3 + 66 * U) * (60 + np.abs(x).sum(1, keepdims=True))
+    assert (np.abs(_np(hid) - r_hid) <= 33 * e).all()
+
+
 def test_cells_agree_with_the_renderers_network(torch):
     """sigma and rgb of one KiloNeRF frame: each ray marched by hand through nerf_test_march's live samples,
     nerf_expert_sort and nerf_cells_forward composites to nerf_render's colour."""
@@ -584,6 +618,61 @@ def test_two_steps_on_two_streams_and_a_captured_one(torch):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(steps[0].results(), want[1]))
     assert all(torch.equal(a, b) for a, b in zip(steps[1].results(), want[1]))
+
+
+def test_every_operator_in_a_graph(torch):
+    """Each call captured on a side stream, with its inputs changed before the replay: what an eager call on
+    those inputs gives; at sizes of the one-launch and the many-launch forms, clusters among them."""
+    import neural_radiance_field_b200 as nb
+    f32, i32 = torch.float32, torch.int32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    def check(ins, outs, call):
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        call()
+        with torch.cuda.graph(graph, stream=st):
+            call()
+        for t in ins:
+            t.copy_(t.flip(0).clone())
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.fill_(-3)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+    for n, k, e in ((20, 8, 300), (40000, 2, 4096)):
+        ids = torch.randint(0, e, (n, k), generator=g, device="cuda", dtype=i32)
+        off, order, pos = torch.empty(e + 1, device="cuda", dtype=i32), torch.empty(n * k, device="cuda", dtype=i32), torch.empty(n, k, device="cuda", dtype=i32)
+        work = torch.empty(nb.nerf_expert_sort_workspace(n, k, e), device="cuda", dtype=torch.uint8)
+        check([ids], [off, order, pos], (lambda: nb.nerf_expert_sort(ids, e, off, order, pos, work)))
+        x, rows, w, out, dw = rnd(n, 36), rnd(n * k, 36), rnd(n, k), rnd(n, 36), rnd(n, k)
+        check([x, w], [rows], (lambda: nb.nerf_expert_dispatch(x, pos, rows, w)))
+        check([rows, w], [out], (lambda: nb.nerf_expert_combine(rows, pos, out, w)))
+        check([rows, x], [out, dw], (lambda: nb.nerf_expert_dispatch_backward(rows, x, pos, out, w, dw)))
+        dr = rnd(n * k, 36)
+        check([rows, x], [dr, dw], (lambda: nb.nerf_expert_combine_backward(x, rows, pos, dr, w, dw)))
+    for n, e, dt in ((30, 100, f32), (2000, 4096, torch.bfloat16), (400, 40000, f32), (9, 130000, torch.float16), (3, 300000, f32)):
+        s, tl = rnd(n, e).to(dt), rnd(n, 5)
+        ti = torch.randint(0, e, (n, 5), generator=g, device="cuda", dtype=i32)
+        loss, grad = torch.empty(n, device="cuda"), torch.empty(n, e, device="cuda", dtype=dt)
+        check([s, tl, ti], [loss, grad], (lambda: nb.nerf_distill_topk(s, tl, ti, 1.3, loss, grad)))
+    n, e = 3000, 20
+    x, d, dr, w = rnd(n, 3), rnd(n, 3), rnd(n, 4), rnd(e, 3317) / 6
+    off = torch.linspace(0, n, e + 1, device="cuda").int()
+    raw, hid, grad = rnd(n, 4), rnd(n, 64), torch.empty(e, 3317, device="cuda")
+    work = torch.empty(nb.nerf_cells_backward_workspace(n, e), device="cuda", dtype=torch.uint8)
+    check([x, d, w], [raw, hid], (lambda: nb.nerf_cells_forward(x, d, off, w, raw, hid)))
+    check([x, d, dr], [grad], (lambda: nb.nerf_cells_backward(x, d, off, w, hid, dr, grad, work)))
 
 
 def test_a_gate_learns_from_its_teachers_top_logits(torch):
