@@ -7,11 +7,10 @@
 // More: three launches over one contiguous chunk of pairs per CTA.
 //   count:   the chunk's pairs of every expert (shared-memory atomics) -> table
 //   columns: for every expert the prefix over the chunks, and its total
-//   place:   the experts' offsets (each CTA scans the totals itself); then, a
-//            tile of the chunk at a time, every warp counts its own run of the
+//   place:   a tile of the chunk at a time, every warp counts its own run of the
 //            tile (16-bit counters, two experts a word), the counts are scanned
-//            over the warps, and every warp walks its run in order, 32 pairs at
-//            a time. A match instruction finds which of the 32 share an expert (a
+//            over the warps (and, before the first tile's, the totals over the
+//            experts), and every warp walks its run in order, 32 pairs at a time. A match instruction finds which of the 32 share an expert (a
 //            ballot per bit of the id took longer), a pair's rank among them is
 //            the number of lower lanes, and the expert's counter advances by
 //            their number. Rows come out in pair order whatever the timing.
@@ -25,14 +24,14 @@ constexpr int ES_WARPS = 16, ES_T = ES_WARPS * 32;
 constexpr int ES_RUN = 4064;                 // pairs of a warp's run in one tile
 constexpr int ES_TILE = ES_WARPS * ES_RUN;
 static_assert(ES_TILE < 65536 && ES_RUN % 32 == 0, "a tile's counts are 16-bit");
-constexpr int ES_MOST_CTAS = 148 * 3;
+constexpr int ES_MOST_CTAS = 148 * 2, ES_PER = (ES_MOST_CTAS + 15) / 16;
 constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
 struct SortPlan {
   int ctas;
   int64_t chunk;                             // pairs of a CTA, a multiple of ES_T
 };
-// Small tables leave room for three CTAs to an SM; a CTA has 2048 pairs at least,
+// Small tables leave room for two CTAs to an SM; a CTA has 2048 pairs at least,
 // or the tables would outgrow the pairs.
 SortPlan sort_plan(int64_t pairs, int n_experts) {
   const int64_t most = n_experts <= 1024 ? ES_MOST_CTAS : 148, want = (pairs + 2047) / 2048;
@@ -97,6 +96,7 @@ __global__ void __launch_bounds__(ES_CT)
 sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   int32_t* __restrict__ table) {
   extern __shared__ int32_t hist[];
+  cudaTriggerProgrammaticLaunchCompletion();
   for (int e = threadIdx.x; e < n_experts; e += ES_CT) hist[e] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
@@ -109,13 +109,15 @@ sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
 
 // lane = expert, warp = a run of chunks: table becomes the exclusive prefix over
 // the chunks, totals the experts' sums
-constexpr int ES_PER = (ES_MOST_CTAS + 31) / 32;
-__global__ void __launch_bounds__(1024)
+constexpr int ES_COL_WARPS = 16;
+__global__ void __launch_bounds__(ES_COL_WARPS * 32, 2)
 sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int32_t* __restrict__ totals) {
-  __shared__ int32_t part[32][33];
+  __shared__ int32_t part[ES_COL_WARPS][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
-  const int per = (chunks + 31) / 32, c0 = min(chunks, warp * per), n = min(chunks, c0 + per) - c0;
+  const int per = (chunks + ES_COL_WARPS - 1) / ES_COL_WARPS, c0 = min(chunks, warp * per), n = min(chunks, c0 + per) - c0;
   int32_t* col = table + (int64_t)c0 * n_experts + e;
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();           // the counts
   int32_t v[ES_PER], sum = 0;
 #pragma unroll
   for (int c = 0; c < ES_PER; ++c) {
@@ -126,9 +128,9 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
   __syncthreads();
   int32_t run = 0;
 #pragma unroll
-  for (int w = 0; w < 31; ++w) run += w < warp ? part[w][lane] : 0;
+  for (int w = 0; w < ES_COL_WARPS - 1; ++w) run += w < warp ? part[w][lane] : 0;
   if (e < n_experts) {
-    if (warp == 31) totals[e] = run + sum;
+    if (warp == ES_COL_WARPS - 1) totals[e] = run + sum;
 #pragma unroll
     for (int c = 0; c < ES_PER; ++c) {
       if (c < n) col[(int64_t)c * n_experts] = run;
@@ -137,7 +139,8 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
   }
 }
 
-__global__ void __launch_bounds__(ES_T)
+// 64 registers, so that its CTAs fit beside those of the launches before it
+__global__ void __launch_bounds__(ES_T, 2)
 sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   const int32_t* __restrict__ table, const int32_t* __restrict__ totals,
                   int32_t* __restrict__ offset, int32_t* __restrict__ order, int32_t* __restrict__ pos) {
@@ -151,36 +154,6 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
   uint32_t* counts = reinterpret_cast<uint32_t*>(sm + n_experts);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   uint32_t* mine = counts + warp * words;
-  {
-    // exclusive scan of the totals, eight experts a thread
-    int32_t v[8], before[8], tot = 0;        // before: the chunks before this one
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = 8 * t + j < n_experts;
-      v[j] = in ? totals[8 * t + j] : 0;
-      before[j] = in ? table[(int64_t)blockIdx.x * n_experts + 8 * t + j] : 0;
-      tot += v[j];
-    }
-    int32_t run = tot;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += u;
-    }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    run -= tot;
-    for (int w = 0; w < warp; ++w) run += sums[w];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (8 * t + j < n_experts) {
-        base[8 * t + j] = run + before[j];
-        if (blockIdx.x == 0) offset[8 * t + j] = run;
-      }
-      run += v[j];
-    }
-    if (blockIdx.x == 0 && t == ES_T - 1) offset[n_experts] = run;
-  }
   const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
   for (int64_t tile = begin; tile < end; tile += ES_TILE) {
     const int64_t left = min((int64_t)ES_TILE, end - tile);
@@ -192,6 +165,37 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
       if ((unsigned)id < (unsigned)n_experts)
         atomicAdd(&mine[id < words ? id : id - words], id < words ? 1u : 1u << 16);
     });
+    if (tile == begin) {
+      cudaGridDependencySynchronize();       // the table and totals; the first tile's counts needed neither
+      // exclusive scan of the totals, eight experts a thread
+      int32_t v[8], before[8], tot = 0;        // before: the chunks before this one
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = 8 * t + j < n_experts;
+        v[j] = in ? totals[8 * t + j] : 0;
+        before[j] = in ? table[(int64_t)blockIdx.x * n_experts + 8 * t + j] : 0;
+        tot += v[j];
+      }
+      int32_t first = tot;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, first, o);
+        if (lane >= o) first += u;
+      }
+      if (lane == 31) sums[warp] = first;
+      __syncthreads();
+      first -= tot;
+      for (int w = 0; w < warp; ++w) first += sums[w];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (8 * t + j < n_experts) {
+          base[8 * t + j] = first + before[j];
+          if (blockIdx.x == 0) offset[8 * t + j] = first;
+        }
+        first += v[j];
+      }
+      if (blockIdx.x == 0 && t == ES_T - 1) offset[n_experts] = first;
+    }
     __syncthreads();
     // counts -> exclusive prefix over the warps, two experts a word
     uint32_t all[ES_WORDS];
@@ -253,6 +257,22 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
   }
 }
 
+// A launch that need not wait for the launch before it in the stream to end.
+template <typename K, typename... Args>
+cudaError_t launch_early(K kernel, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 int64_t table_ints(const SortPlan& p, int n_experts) { return (int64_t)p.ctas * n_experts + n_experts; }
 
 }  // namespace
@@ -272,14 +292,18 @@ cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts,
   int32_t* table = (int32_t*)work;
   int32_t* totals = table + (int64_t)plan.ctas * n_experts;
   const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
-  sort_count_kernel<<<plan.ctas, ES_CT, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
-  sort_columns_kernel<<<(n_experts + 31) / 32, 1024, 0, st>>>(table, plan.ctas, n_experts, totals);
-  const cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
+  cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
   if (e != cudaSuccess) return e;
-  sort_place_kernel<<<plan.ctas, ES_T, place_sm, st>>>(ids, pairs, plan.chunk, n_experts, table, totals, offset, order,
-                                                       pos);
-  return cudaGetLastError();
+  sort_count_kernel<<<plan.ctas, ES_CT, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
+  // each of the other two may start while the one before it runs, and waits for
+  // its results itself
+  e = launch_early(sort_columns_kernel, (n_experts + 31) / 32, ES_COL_WARPS * 32, 0, st, table, plan.ctas, n_experts,
+                   totals);
+  if (e != cudaSuccess) return e;
+  e = launch_early(sort_place_kernel, plan.ctas, ES_T, place_sm, st, ids, pairs, plan.chunk, n_experts,
+                   (const int32_t*)table, (const int32_t*)totals, offset, order, pos);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace nerfb
