@@ -804,6 +804,7 @@ __global__ void __launch_bounds__(CB_THREADS, 1) cells_backward_kernel(CellsBack
   extern __shared__ __align__(16) uint8_t cells_sm[];
   CellsBackwardShared& S = *reinterpret_cast<CellsBackwardShared*>(cells_sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cudaTriggerProgrammaticLaunchCompletion();
   unit_prefix<CB_THREADS>(P.offset, P.n, P.n_cells, CB_ROWS, S.first);
   if (blockIdx.x == 0)
     for (int c = tid; c <= P.n_cells; c += CB_THREADS) P.first_out[c] = S.first[c];
@@ -861,14 +862,22 @@ __device__ __forceinline__ void join_parts(int u0, int u1, int units, int ctas, 
     if (256 * i + (int)threadIdx.x < N) out[256 * i + threadIdx.x] = s[i];
 }
 __global__ void __launch_bounds__(256)
-cells_join_kernel(const int* __restrict__ first, int n_cells, int ctas, const float* __restrict__ parts_a,
-                  const float* __restrict__ parts_b, float* __restrict__ grad) {
-  const int cell = blockIdx.x, u0 = first[cell] + 1, u1 = first[cell + 1], units = first[n_cells];
+cells_join_kernel(const int32_t* __restrict__ offset, int64_t n, const int* __restrict__ first, int n_cells, int ctas,
+                  const float* __restrict__ parts_a, const float* __restrict__ parts_b, float* __restrict__ grad) {
+  const int cell = blockIdx.x;
   float* __restrict__ G = grad + (int64_t)cell * CELL_NP;
-  if (u0 >= u1) {
-    for (int q = threadIdx.x; q < CELL_NP; q += 256) G[q] = 0.0f;
-    return;
+  const int64_t lo = min(max((int64_t)offset[cell], (int64_t)0), n), hi = min(max((int64_t)offset[cell + 1], (int64_t)0), n);
+  if (hi <= lo) {                            // a blob starts at any float: 16-byte stores from its first 16-byte boundary
+    const int head = (int)((0 - (uintptr_t)G) % 16 / 4), vecs = (CELL_NP - head) / 4;
+    for (int q = threadIdx.x; q < vecs; q += 256)
+      reinterpret_cast<float4*>(G + head)[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int rest = CELL_NP - 4 * vecs;     // before the vectors and after them
+    if ((int)threadIdx.x < rest) G[(int)threadIdx.x < head ? threadIdx.x : threadIdx.x + 4 * vecs] = 0.0f;
   }
+  cudaGridDependencySynchronize();           // the gradients and their parts; the zeros did not need them
+  if (hi <= lo) return;
+  const int u0 = first[cell] + 1, u1 = first[cell + 1], units = first[n_cells];
+  if (u0 >= u1) return;
   join_parts<CB_NA, CB_A>(u0, u1, units, ctas, parts_a, G);
   join_parts<CB_NB, CB_B>(u0, u1, units, ctas, parts_b, G + O_W2);
 }
@@ -906,8 +915,10 @@ cudaError_t launch_cells_backward(const float* x, const float* d, int64_t n, con
   float* parts_b = parts_a + (int64_t)ctas * CB_A * 2 * CB_NA;
   const CellsBackwardArgs P{x, d, n, offset, n_cells, cell_w, hidden, d_raw, grad, first, parts_a, parts_b};
   cells_backward_kernel<<<ctas, CB_THREADS, sm, st>>>(P);
-  cells_join_kernel<<<n_cells, 256, 0, st>>>(first, n_cells, ctas, parts_a, parts_b, grad);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_early(cells_join_kernel, n_cells, 256, 0, st, offset, n, (const int*)first, n_cells, ctas,
+                      (const float*)parts_a, (const float*)parts_b, grad);
 }
 
 }  // namespace nerfb

@@ -7,11 +7,10 @@
 // point and holds the point's own row in registers while its k sorted rows pass,
 // so the point's row moves once whatever k is, and the weight gradient comes from
 // the vectors that the row's own pass has in registers. A group is the power of
-// two that covers the row, but no wider than 128 bytes (a full line a step): its
-// lanes then take several vectors of a wide row at once, which keeps more loads
-// in flight and spreads the pair's index work over them. Rows move in 16-byte vectors where their
-// size and both buffers allow it, in 4-byte words where those do, else by
-// element.
+// two that covers the row, but no wider than 64 to 128 bytes: its lanes then
+// take several vectors of a wide row at once, which keeps more loads in flight
+// and spreads the pair's index work over them. Rows move in vectors of 16, 8 or 4 bytes,
+// the widest that their size and the buffers allow, else by element.
 #include "nerf_experts.cuh"
 #include "nerf_vec.cuh"
 
@@ -135,7 +134,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
                    const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
                    T* __restrict__ out, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
-  constexpr int U = KC == 2 ? 4 : 1;                  // vectors of a row that a lane has in flight
+  constexpr int U = KC == 2 || BYTES <= 4 ? 4 : KC == 4 ? 2 : 1;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
   const bool on = i < n;
@@ -241,22 +240,25 @@ void run(const RowArgs& A) {
     rows_gather_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
                                                                 A.k, A.w, (T*)A.out, A.dw);
 }
-// pairs in chunks of two for k <= 2, else of eight: an unused place of a chunk
-// costs its predicates, and a chunk's rows are all in flight at once
+// pairs in chunks of two for k <= 2, of four for k <= 4, else of eight: an unused
+// place of a chunk costs its predicates, and a chunk's rows are all in flight at once
 template <bool SCATTER, typename T, int BYTES>
 void run_k(const RowArgs& A) {
   if (A.k <= 2) A.dw ? run<SCATTER, T, BYTES, 2, true>(A) : run<SCATTER, T, BYTES, 2, false>(A);
+  else if (A.k <= 4) A.dw ? run<SCATTER, T, BYTES, 4, true>(A) : run<SCATTER, T, BYTES, 4, false>(A);
   else A.dw ? run<SCATTER, T, BYTES, 8, true>(A) : run<SCATTER, T, BYTES, 8, false>(A);
 }
 template <bool SCATTER, typename T>
 cudaError_t run_t(RowArgs A, int width) {
   const uintptr_t all = (uintptr_t)A.a | (uintptr_t)A.b | (uintptr_t)A.out | (uintptr_t)(width * sizeof(T));
-  const int bytes = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)sizeof(T);
+  const int bytes = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : (int)sizeof(T);
   A.nv = (int)(width * sizeof(T)) / bytes;
-  const int widest = bytes == 16 ? 8 : 32;
+  // rows of small words: a lane takes four of them, rows of one to four a lane alone
+  const int widest = bytes >= 8 ? 8 : 16, lanes = bytes >= 8 ? A.nv : (A.nv + 3) / 4;
   A.G = 1;
-  while (A.G < A.nv && A.G < widest) A.G *= 2;
+  while (A.G < lanes && A.G < widest) A.G *= 2;
   if (bytes == 16) run_k<SCATTER, T, 16>(A);
+  else if (bytes == 8) run_k<SCATTER, T, 8>(A);
   else if (bytes == 4) run_k<SCATTER, T, 4>(A);
   else run_k<SCATTER, T, (int)sizeof(T)>(A);
   return cudaGetLastError();

@@ -257,22 +257,6 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
   }
 }
 
-// A launch that need not wait for the launch before it in the stream to end.
-template <typename K, typename... Args>
-cudaError_t launch_early(K kernel, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 int64_t table_ints(const SortPlan& p, int n_experts) { return (int64_t)p.ctas * n_experts + n_experts; }
 
 }  // namespace

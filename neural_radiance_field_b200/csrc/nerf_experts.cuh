@@ -37,4 +37,22 @@ cudaError_t launch_cells_backward(const float* x, const float* d, int64_t n, con
                                   int n_cells, const float* cell_w, const float* hidden,
                                   const float* d_raw, float* grad, void* work, cudaStream_t st);
 
+// A launch that may start while the launch before it in the stream still runs. Its
+// kernel waits for that one's end (cudaGridDependencySynchronize) in every block
+// before it reads a result of it, writes what it reads, or ends.
+template <typename K, typename... Args>
+cudaError_t launch_early(K kernel, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace nerfb

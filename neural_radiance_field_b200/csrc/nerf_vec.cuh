@@ -84,7 +84,7 @@ __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
   return r;
 }
 
-// N elements of T in one load or store of 16, 4 or 2 bytes, held as 32-bit words
+// N elements of T in one load or store of 16, 8, 4 or 2 bytes, held as 32-bit words
 // (kept as single 16-bit elements they would take a register each).
 template <typename T, int BYTES>
 struct Vec {
@@ -95,6 +95,9 @@ struct Vec {
     if constexpr (BYTES == 16) {
       const uint4 r = __ldg(reinterpret_cast<const uint4*>(p) + v);
       words[0] = r.x, words[1 % W] = r.y, words[2 % W] = r.z, words[3 % W] = r.w;
+    } else if constexpr (BYTES == 8) {
+      const uint2 r = __ldg(reinterpret_cast<const uint2*>(p) + v);
+      words[0] = r.x, words[1 % W] = r.y;
     } else if constexpr (BYTES == 4) {
       words[0] = __ldg(reinterpret_cast<const uint32_t*>(p) + v);
     } else {
@@ -104,6 +107,8 @@ struct Vec {
   __device__ __forceinline__ void store(void* p, int64_t v) const {
     if constexpr (BYTES == 16)
       reinterpret_cast<uint4*>(p)[v] = make_uint4(words[0], words[1 % W], words[2 % W], words[3 % W]);
+    else if constexpr (BYTES == 8)
+      reinterpret_cast<uint2*>(p)[v] = make_uint2(words[0], words[1 % W]);
     else if constexpr (BYTES == 4)
       reinterpret_cast<uint32_t*>(p)[v] = words[0];
     else
