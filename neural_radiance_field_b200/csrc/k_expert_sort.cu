@@ -14,6 +14,11 @@
 //            ballot per bit of the id took longer), a pair's rank among them is
 //            the number of lower lanes, and the expert's counter advances by
 //            their number. Rows come out in pair order whatever the timing.
+// The launches overlap: place counts its first tile while columns still runs.
+//
+// 6.3 M pairs over 4,096 experts: 58 us, 1.3 TB/s of the 75 MB that the sort has
+// to read and write (0.20 of the copy rate). Place (about 40 us alone) is bound by
+// the match, 32 cycles of an SM for 32 pairs; count takes 10 us, columns 5.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
