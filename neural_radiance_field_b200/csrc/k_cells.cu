@@ -36,8 +36,9 @@ namespace nerfb {
 namespace {
 
 // parameter offsets inside a cell's blob
-constexpr int O_B1 = 2016, O_W2 = 2048, O_B2 = 3072, O_WS = 3104, O_BS = 3136, O_WC = 3137,
-              O_BC = 3314;
+constexpr int O_B1 = 32 * 63, O_W2 = O_B1 + 32, O_B2 = O_W2 + 32 * 32, O_WS = O_B2 + 32, O_BS = O_WS + 32,
+              O_WC = O_BS + 1, O_BC = O_WC + 3 * 59;
+static_assert(O_BC + 3 == CELL_NP, "the blob's parts");
 
 __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -851,9 +852,10 @@ __global__ void __launch_bounds__(CB_THREADS, 1) cells_backward_kernel(CellsBack
 }
 
 // One CTA per cell: nothing where one warp wrote it, zeros where it has no rows,
-// the sum of its parts in warp order where several did; for each role.
+// the sum of its parts in warp order where several did; for each role. `first` and
+// the parts are written while this kernel may already run: no non-coherent loads.
 template <int N, int WARPS>
-__device__ __forceinline__ void join_parts(int u0, int u1, int units, int ctas, const float* __restrict__ parts,
+__device__ __forceinline__ void join_parts(int u0, int u1, int units, int ctas, const float* parts,
                                            float* __restrict__ out) {
   const int per = (units + ctas * WARPS - 1) / (ctas * WARPS), w0 = u0 / per, w1 = (u1 - 1) / per;
   if (w0 == w1) return;
@@ -873,8 +875,8 @@ __device__ __forceinline__ void join_parts(int u0, int u1, int units, int ctas, 
     if (256 * i + (int)threadIdx.x < N) out[256 * i + threadIdx.x] = s[i];
 }
 __global__ void __launch_bounds__(256)
-cells_join_kernel(const int32_t* __restrict__ offset, int64_t n, const int* __restrict__ first, int n_cells, int ctas,
-                  const float* __restrict__ parts_a, const float* __restrict__ parts_b, float* __restrict__ grad) {
+cells_join_kernel(const int32_t* __restrict__ offset, int64_t n, const int* first, int n_cells, int ctas,
+                  const float* parts_a, const float* parts_b, float* __restrict__ grad) {
   const int cell = blockIdx.x;
   float* __restrict__ G = grad + (int64_t)cell * CELL_NP;
   const int64_t lo = min(max((int64_t)offset[cell], (int64_t)0), n), hi = min(max((int64_t)offset[cell + 1], (int64_t)0), n);
@@ -887,7 +889,7 @@ cells_join_kernel(const int32_t* __restrict__ offset, int64_t n, const int* __re
   }
   cudaGridDependencySynchronize();           // the gradients and their parts; the zeros did not need them
   if (hi <= lo) return;
-  const int u0 = first[cell] + 1, u1 = first[cell + 1], units = first[n_cells];
+  const int u0 = __ldcg(first + cell) + 1, u1 = __ldcg(first + cell + 1), units = __ldcg(first + n_cells);
   if (u0 >= u1) return;
   join_parts<CB_NA, CB_A>(u0, u1, units, ctas, parts_a, G);
   join_parts<CB_NB, CB_B>(u0, u1, units, ctas, parts_b, G + O_W2);

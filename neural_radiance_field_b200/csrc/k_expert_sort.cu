@@ -10,10 +10,11 @@
 //   place:   a tile of the chunk at a time, every warp counts its own run of the
 //            tile (16-bit counters, two experts a word), the counts are scanned
 //            over the warps (and, before the first tile's, the totals over the
-//            experts), and every warp walks its run in order, 32 pairs at a time. A match instruction finds which of the 32 share an expert (a
-//            ballot per bit of the id took longer), a pair's rank among them is
-//            the number of lower lanes, and the expert's counter advances by
-//            their number. Rows come out in pair order whatever the timing.
+//            experts), and every warp walks its run in order, 32 pairs at a time.
+//            A match instruction finds which of the 32 share an expert (a ballot
+//            per bit of the id took longer), a pair's rank among them is the
+//            number of lower lanes, and the expert's counter advances by their
+//            number. Rows come out in pair order whatever the timing.
 // The launches overlap: place counts its first tile while columns still runs.
 //
 // 6.3 M pairs over 4,096 experts: 58 us, 1.3 TB/s of the 75 MB that the sort has
@@ -116,7 +117,7 @@ sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
 // the chunks, totals the experts' sums
 constexpr int ES_COL_WARPS = 16;
 __global__ void __launch_bounds__(ES_COL_WARPS * 32, 2)
-sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int32_t* __restrict__ totals) {
+sort_columns_kernel(int32_t* table, int chunks, int n_experts, int32_t* totals) {
   __shared__ int32_t part[ES_COL_WARPS][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
   const int per = (chunks + ES_COL_WARPS - 1) / ES_COL_WARPS, c0 = min(chunks, warp * per), n = min(chunks, c0 + per) - c0;
@@ -126,7 +127,7 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
   int32_t v[ES_PER], sum = 0;
 #pragma unroll
   for (int c = 0; c < ES_PER; ++c) {
-    v[c] = c < n && e < n_experts ? col[(int64_t)c * n_experts] : 0;
+    v[c] = c < n && e < n_experts ? __ldcg(col + (int64_t)c * n_experts) : 0;
     sum += v[c];
   }
   part[warp][lane] = sum;
@@ -147,7 +148,7 @@ sort_columns_kernel(int32_t* __restrict__ table, int chunks, int n_experts, int3
 // 64 registers, so that its CTAs fit beside those of the launches before it
 __global__ void __launch_bounds__(ES_T, 2)
 sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
-                  const int32_t* __restrict__ table, const int32_t* __restrict__ totals,
+                  const int32_t* table, const int32_t* totals,
                   int32_t* __restrict__ offset, int32_t* __restrict__ order, int32_t* __restrict__ pos) {
   // base[e]: the next sorted row of expert e for this CTA; words of two 16-bit
   // counters, [warp][words]: word w counts experts w (low half) and words + w (two
@@ -172,13 +173,14 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
     });
     if (tile == begin) {
       cudaGridDependencySynchronize();       // the table and totals; the first tile's counts needed neither
-      // exclusive scan of the totals, eight experts a thread
+      // exclusive scan of the totals, eight experts a thread. Both arrays are written
+      // while this kernel may already run: loads from L2, never the non-coherent ones
       int32_t v[8], before[8], tot = 0;        // before: the chunks before this one
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool in = 8 * t + j < n_experts;
-        v[j] = in ? totals[8 * t + j] : 0;
-        before[j] = in ? table[(int64_t)blockIdx.x * n_experts + 8 * t + j] : 0;
+        v[j] = in ? __ldcg(totals + 8 * t + j) : 0;
+        before[j] = in ? __ldcg(table + (int64_t)blockIdx.x * n_experts + 8 * t + j) : 0;
         tot += v[j];
       }
       int32_t first = tot;

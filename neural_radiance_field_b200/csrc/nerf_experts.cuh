@@ -39,7 +39,8 @@ cudaError_t launch_cells_backward(const float* x, const float* d, int64_t n, con
 
 // A launch that may start while the launch before it in the stream still runs. Its
 // kernel waits for that one's end (cudaGridDependencySynchronize) in every block
-// before it reads a result of it, writes what it reads, or ends.
+// before it reads a result of it, writes what it reads, or ends; and it takes those
+// results without const __restrict__, whose loads assume data that no one writes.
 template <typename K, typename... Args>
 cudaError_t launch_early(K kernel, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg{};

@@ -104,6 +104,26 @@ def test_sort_of_many_tiles(torch, n, k, e):
     assert torch.equal(pos.reshape(-1).long(), torch.where(key < e, place, -1))
 
 
+@pytest.mark.parametrize("n,k,e", [(60000, 2, 33), (60000, 2, 1000), (60000, 2, 4095)])
+def test_sorts_back_to_back_share_a_workspace(torch, n, k, e):
+    """Launch follows launch with other ids and one workspace, expert counts that no 32 divide."""
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng([n, k, e])
+    all_ids = [_ids(rng, n, k, e, drop) for drop in (0.0, 0.3, 0.7)]
+    ids = [_cuda(torch, i) for i in all_ids]
+    work = torch.empty(nb.nerf_expert_sort_workspace(n, k, e), device="cuda", dtype=torch.uint8)
+    outs = [(torch.empty(e + 1, device="cuda", dtype=torch.int32), torch.empty((n, k), device="cuda", dtype=torch.int32))
+            for _ in range(60)]
+    for r, (off, pos) in enumerate(outs):
+        nb.nerf_expert_sort(ids[r % 3], e, off, None, pos, work)
+    torch.cuda.synchronize()
+    for r in range(3):
+        off, _, pos = E.sort(all_ids[r], e)
+        for got_off, got_pos in outs[r::3]:
+            np.testing.assert_array_equal(got_off.cpu().numpy(), off)
+            np.testing.assert_array_equal(got_pos.cpu().numpy(), pos)
+
+
 def test_sort_agrees_with_the_cell_router(torch):
     """One cell per point: the same counts and cells as nerf_test_route_cells."""
     import neural_radiance_field_b200 as nb
@@ -441,6 +461,35 @@ def test_cells(torch, name):
     again = torch.full_like(grad, -3.0)
     nb.nerf_cells_backward(xt, dt, ot, wt, hid, gt, again, work)
     assert torch.equal(grad, again)
+
+
+def test_cell_gradients_back_to_back_share_a_workspace(torch):
+    """Launch follows launch with other rows per cell and one workspace: every result is that of the call alone."""
+    import neural_radiance_field_b200 as nb
+    cases, n = [], 4000
+    for seed, counts in enumerate(([4000], [7, 0, 1993, 2000], [100] * 40)):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+        counts = counts + [0] * (41 - len(counts))
+        off = _cuda(torch, np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+        x, d, w, d_raw = rnd(n, 3), rnd(n, 3), rnd(41, 3317) * 0.1, rnd(n, 4)
+        raw, hidden = torch.empty(n, 4, device="cuda"), torch.empty(n, 64, device="cuda")
+        nb.nerf_cells_forward(x, d, off, w, raw, hidden)
+        cases.append((x, d, off, w, hidden, d_raw))
+    size = nb.nerf_cells_backward_workspace(n, 41)
+    alone = []
+    for c in cases:
+        g = torch.full((41, 3317), float("nan"), device="cuda")
+        nb.nerf_cells_backward(*c, g, torch.zeros(size, device="cuda", dtype=torch.uint8))
+        torch.cuda.synchronize()
+        assert torch.isfinite(g).all()
+        alone.append(g)
+    work = torch.empty(size, device="cuda", dtype=torch.uint8)
+    outs = [torch.full((41, 3317), float("nan"), device="cuda") for _ in range(30)]
+    for r, g in enumerate(outs):
+        nb.nerf_cells_backward(*cases[r % 3], g, work)
+    for r, g in enumerate(outs):
+        assert torch.equal(g, alone[r % 3])
 
 
 def test_cells_far_positions(torch):

@@ -90,7 +90,7 @@ def test_cells_gradient_against_differences():
     def loss(w):
         return (E.cells_forward(x, d, offset, w)[0] * g).sum()
 
-    for q in list(rng.integers(0, E.N_CELL, size=150)) + [2016, 3072, 3104, 3136, 3137, 3314, 3316]:
+    for q in list(rng.integers(0, E.N_CELL, size=150)) + [2016, 2048, 2048 + 32 * 32, 3104, 3136, 3137, 3314, 3316]:
         for c in (0, 2):
             hi, lo = w.copy(), w.copy()
             hi[c, q] += 1e-6
