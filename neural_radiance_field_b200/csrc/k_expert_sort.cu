@@ -1,8 +1,11 @@
 // Stable counting sort of (point, expert) pairs by expert.
 //
-// Up to 1024 pairs: one CTA; a pair's sorted row is the number of kept pairs
+// Few pairs (ES_SMALL): one CTA; a pair's sorted row is the number of kept pairs
 // before it in (expert, pair) order, counted directly (the ids sit in shared
 // memory), and the offsets come from a binary search. One launch.
+//
+// Up to ES_ALONE: the place kernel below alone, in one CTA whose counts are the
+// totals too. One launch.
 //
 // More: three launches over one contiguous chunk of pairs per CTA.
 //   count:   the chunk's pairs of every expert (shared-memory atomics) -> table
@@ -25,11 +28,21 @@
 namespace nerfb {
 namespace {
 
-constexpr int ES_SMALL = 1024;
+// its work grows with the square of the pairs: 128 pairs of 64 experts take 2.6 us
+// against 3.6 in the place kernel, 256 pairs 4.2 against 3.7
+constexpr int ES_SMALL = 128, ES_SMALL_T = 1024;
 constexpr int ES_WARPS = 16, ES_T = ES_WARPS * 32;
 constexpr int ES_RUN = 4064;                 // pairs of a warp's run in one tile
 constexpr int ES_TILE = ES_WARPS * ES_RUN;
 static_assert(ES_TILE < 65536 && ES_RUN % 32 == 0, "a tile's counts are 16-bit");
+// Pairs that one CTA sorts alone: 4,096 take 9.0 us against the three launches' 10.9
+// with 4,096 experts and 8.5 against 7.7 with 64, where two launches less weigh more
+// for the caller; 8,192 pairs of 64 experts 13.4 against 7.8.
+constexpr int ES_ALONE = 4096;
+static_assert(ES_ALONE <= ES_TILE, "in one tile");
+// Pairs of a CTA at least, one per thread: 16,384 pairs of 64 experts take 7.0 us,
+// with 1,024 to a CTA 7.9 and with 2,048 9.2.
+constexpr int ES_CHUNK = ES_T;
 constexpr int ES_MOST_CTAS = 148 * 2, ES_PER = (ES_MOST_CTAS + 15) / 16;
 constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
@@ -37,16 +50,16 @@ struct SortPlan {
   int ctas;
   int64_t chunk;                             // pairs of a CTA, a multiple of ES_T
 };
-// Small tables leave room for two CTAs to an SM; a CTA has 2048 pairs at least,
-// or the tables would outgrow the pairs.
+// Small tables leave room for two CTAs to an SM (6.3 M pairs of 1,000 experts take
+// 75 us, with one 120; of 64 experts 66 and 64).
 SortPlan sort_plan(int64_t pairs, int n_experts) {
-  const int64_t most = n_experts <= 1024 ? ES_MOST_CTAS : 148, want = (pairs + 2047) / 2048;
+  const int64_t most = n_experts <= 1024 ? ES_MOST_CTAS : 148, want = (pairs + ES_CHUNK - 1) / ES_CHUNK;
   const int64_t ctas = want < most ? want : most;
   const int64_t chunk = ((pairs + ctas - 1) / ctas + ES_T - 1) / ES_T * ES_T;
   return {(int)((pairs + chunk - 1) / chunk), chunk};
 }
 
-__global__ void __launch_bounds__(ES_SMALL)
+__global__ void __launch_bounds__(ES_SMALL_T)
 sort_small_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts, int32_t* __restrict__ offset,
                   int32_t* __restrict__ order, int32_t* __restrict__ pos) {
   __shared__ __align__(16) int32_t id_s[ES_SMALL];
@@ -73,7 +86,7 @@ sort_small_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts, int
     pos[t] = id != INT32_MAX ? row : -1;
   }
   __syncthreads();
-  for (int e = t; e <= n_experts; e += ES_SMALL) {
+  for (int e = t; e <= n_experts; e += ES_SMALL_T) {
     int lo = 0, hi = kept;                   // the first sorted pair of an expert >= e
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -145,7 +158,9 @@ sort_columns_kernel(int32_t* table, int chunks, int n_experts, int32_t* totals) 
   }
 }
 
-// 64 registers, so that its CTAs fit beside those of the launches before it
+// 64 registers, so that its CTAs fit beside those of the launches before it.
+// ALONE: one CTA has all pairs in one tile, and its own counts are the totals.
+template <bool ALONE>
 __global__ void __launch_bounds__(ES_T, 2)
 sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk, int n_experts,
                   const int32_t* table, const int32_t* totals,
@@ -171,18 +186,12 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
       if ((unsigned)id < (unsigned)n_experts)
         atomicAdd(&mine[id < words ? id : id - words], id < words ? 1u : 1u << 16);
     });
-    if (tile == begin) {
-      cudaGridDependencySynchronize();       // the table and totals; the first tile's counts needed neither
-      // exclusive scan of the totals, eight experts a thread. Both arrays are written
-      // while this kernel may already run: loads from L2, never the non-coherent ones
-      int32_t v[8], before[8], tot = 0;        // before: the chunks before this one
+    // base and offset from the totals v of the thread's eight experts, 8 t .. 8 t + 7, and
+    // before: their pairs in the chunks before this one
+    const auto scan = [&](const int32_t* v, const int32_t* before) {
+      int32_t tot = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = 8 * t + j < n_experts;
-        v[j] = in ? __ldcg(totals + 8 * t + j) : 0;
-        before[j] = in ? __ldcg(table + (int64_t)blockIdx.x * n_experts + 8 * t + j) : 0;
-        tot += v[j];
-      }
+      for (int j = 0; j < 8; ++j) tot += v[j];
       int32_t first = tot;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -202,6 +211,18 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
         first += v[j];
       }
       if (blockIdx.x == 0 && t == ES_T - 1) offset[n_experts] = first;
+    };
+    if (!ALONE && tile == begin) {
+      cudaGridDependencySynchronize();       // the table and totals; the first tile's counts needed neither
+      // both are written while this kernel may already run: loads from L2, never the non-coherent ones
+      int32_t v[8], before[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = 8 * t + j < n_experts;
+        v[j] = in ? __ldcg(totals + 8 * t + j) : 0;
+        before[j] = in ? __ldcg(table + (int64_t)blockIdx.x * n_experts + 8 * t + j) : 0;
+      }
+      scan(v, before);
     }
     __syncthreads();
     // counts -> exclusive prefix over the warps, two experts a word
@@ -217,8 +238,20 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
           counts[w * words + q] = all[u];
           all[u] += v;
         }
+      if (ALONE && q < words) {              // the totals, on their way to the threads that scan them
+        base[q] = all[u] & 0xffffu;
+        if (words + q < n_experts) base[words + q] = all[u] >> 16;
+      }
     }
     __syncthreads();
+    if (ALONE) {
+      int32_t v[8];
+      const int32_t before[8] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 8 * t + j < n_experts ? base[8 * t + j] : 0;
+      scan(v, before);                       // a thread overwrites the entries that it read
+      __syncthreads();
+    }
     const uint32_t lower = (1u << lane) - 1u;
     int ahead[2][4];                         // the ids of the next 256 pairs, on their way
 #pragma unroll
@@ -251,6 +284,7 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
         __syncwarp();
       }
     }
+    if (ALONE) return;
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < ES_WORDS; ++u) {
@@ -269,30 +303,37 @@ int64_t table_ints(const SortPlan& p, int n_experts) { return (int64_t)p.ctas * 
 }  // namespace
 
 int64_t expert_sort_workspace(int64_t pairs, int n_experts) {
-  if (pairs <= ES_SMALL) return 16;
+  if (pairs <= ES_ALONE) return 16;
   return (table_ints(sort_plan(pairs, n_experts), n_experts) * 4 + 15) / 16 * 16;
 }
 
 cudaError_t launch_expert_sort(const int32_t* ids, int64_t pairs, int n_experts, int32_t* offset,
                                int32_t* order, int32_t* pos, void* work, cudaStream_t st) {
   if (pairs <= ES_SMALL) {
-    sort_small_kernel<<<1, ES_SMALL, 0, st>>>(ids, (int)pairs, n_experts, offset, order, pos);
+    sort_small_kernel<<<1, ES_SMALL_T, 0, st>>>(ids, (int)pairs, n_experts, offset, order, pos);
     return cudaGetLastError();
   }
+  constexpr int most_sm = EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2;
+  const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
+  cudaError_t e;
+  if (pairs <= ES_ALONE) {
+    e = cudaFuncSetAttribute(sort_place_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most_sm);
+    if (e != cudaSuccess) return e;
+    sort_place_kernel<true><<<1, ES_T, place_sm, st>>>(ids, pairs, pairs, n_experts, nullptr, nullptr, offset, order, pos);
+    return cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(sort_place_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most_sm);
+  if (e != cudaSuccess) return e;
   const SortPlan plan = sort_plan(pairs, n_experts);
   int32_t* table = (int32_t*)work;
   int32_t* totals = table + (int64_t)plan.ctas * n_experts;
-  const size_t place_sm = (size_t)n_experts * 4 + (size_t)ES_WARPS * ((n_experts + 1) / 2) * 4;
-  cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       EXPERT_MAX * 4 + ES_WARPS * EXPERT_MAX * 2);
-  if (e != cudaSuccess) return e;
   sort_count_kernel<<<plan.ctas, ES_CT, n_experts * 4, st>>>(ids, pairs, plan.chunk, n_experts, table);
   // each of the other two may start while the one before it runs, and waits for
   // its results itself
   e = launch_early(sort_columns_kernel, (n_experts + 31) / 32, ES_COL_WARPS * 32, 0, st, table, plan.ctas, n_experts,
                    totals);
   if (e != cudaSuccess) return e;
-  e = launch_early(sort_place_kernel, plan.ctas, ES_T, place_sm, st, ids, pairs, plan.chunk, n_experts,
+  e = launch_early(sort_place_kernel<false>, plan.ctas, ES_T, place_sm, st, ids, pairs, plan.chunk, n_experts,
                    (const int32_t*)table, (const int32_t*)totals, offset, order, pos);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
