@@ -594,11 +594,20 @@ cudaError_t run_stage(const DistillArgs& A, int C, cudaStream_t st) {
 
 template <typename T, int BYTES>
 cudaError_t run_wide(const DistillArgs& A, cudaStream_t st) {
-  // CTAs of a row: eight, which with 296 CTAs at a time keeps 37 rows in flight
-  // and their second reading in L2; fewer where a part would be below 32 KB
+  // CTAs of a row: eight for few rows (20 rows of 480 KB: 11 us, two CTAs a row 17),
+  // fewer where a part would be below 32 KB (4,096 rows of 16 KB: one CTA 69 us, two
+  // 139), and fewer where that leaves rows enough for all 296 CTAs and the rows in
+  // flight stay in L2 for their second reading (777 rows of 480 KB: four 194 us, two
+  // 202, eight 245; 300 rows of 1.2 MB: eight 261, four 299). Clusters of eight leave
+  // a tenth of the SMs idle, so those give way at more bytes (777 rows of 800 KB:
+  // four 323 us, eight 361).
   const int64_t bytes = (int64_t)A.classes * sizeof(T);
   int C = 8;
-  while (C > 1 && bytes / C < 32768) C /= 2;
+  while (C > 1) {
+    const int64_t held = 296 / (C / 2) * bytes, limit = int64_t(C == 8 ? 80 : 48) << 20;
+    if (bytes / C >= 32768 && (A.n * (C / 2) < 296 || held > limit)) break;
+    C /= 2;
+  }
   const int64_t most = 296 / C;
   return run_clusters(distill_wide_kernel<T, BYTES>, A.n < most ? A.n : most, DW_T, 0, C, st, A, C);
 }
@@ -611,9 +620,11 @@ cudaError_t run_t(const DistillArgs& A, cudaStream_t st) {
   if (bytes <= 512) return run_rows<T, 1>(A, st);
   if (bytes <= 1024) return run_rows<T, 2>(A, st);
   if (bytes <= 4096) return run_rows<T, 8>(A, st);
-  // a warp a row needs some 1200 rows to fill the SMs
-  if (A.n >= 1184 && bytes <= 8192) return run_rows<T, 16>(A, st);
-  if (A.n >= 1184 && bytes <= 16384) return run_rows<T, 32>(A, st);
+  // A warp a row from four rows an SM on: of 592 rows of 8 KB it takes 6.3 us against
+  // the CTA's 7.9, of 16 KB 9.6 against 9.3 (1,184: 6.5 against 13.4, 10.0 against
+  // 16.0); of 148 rows 6.1 against 4.3, 9.4 against 4.9.
+  if (A.n >= 592 && bytes <= 8192) return run_rows<T, 16>(A, st);
+  if (A.n >= 592 && bytes <= 16384) return run_rows<T, 32>(A, st);
   int C = 1;                                 // CTAs of a row
   while (C <= 8 && bytes > (int64_t)DS_PART * C) C *= 2;
   return C <= 8 ? run_stage<T>(A, C, st) : run_wide<T, 16>(A, st);
