@@ -460,7 +460,8 @@ NERF_API nerf_status nerf_expert_combine_backward(const void* d_out, const void*
  * `dtype`, row_scale [n] fp32 (NULL: 1). An entry is kept when its id is in
  * 0..n_classes-1 and its logit is not -inf; a row that keeps none has loss 0
  * and gradient 0. An id given twice counts twice. A student logit of -inf has
- * q = 0 (a row of nothing else has no distribution: NaN). 1 <= k <= 256, 1 <= n_classes <= 2^30, T > 0 and finite. */
+ * q = 0 (a row of nothing else has no distribution: NaN). 1 <= k <= 256,
+ * 1 <= n_classes <= 2^30, 2^-60 <= T <= 2^60. */
 NERF_API nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n, int n_classes,
                                        const float* teacher_logits, const int32_t* teacher_ids,
                                        int k, float temperature, const float* row_scale,

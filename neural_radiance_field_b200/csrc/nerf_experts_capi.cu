@@ -1,5 +1,4 @@
 // The C ABI of the expert operators: argument validation, then one launcher each.
-#include <cmath>
 #include <cstdio>
 
 #include "nerf_experts.cuh"
@@ -154,8 +153,9 @@ nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n, int n_c
   if (n < 1 || n > (int64_t(1) << 40)) return refuse(fn, "n must be in 1..2^40");
   if (n_classes < 1 || n_classes > (1 << 30)) return refuse(fn, "n_classes must be in 1..2^30");
   if (k < 1 || k > DISTILL_MAX_K) return refuse(fn, "k must be in 1..256");
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return refuse(fn, "temperature must be positive and finite");
+  // T, log2(e) / T and T^2 stay normal numbers
+  if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f))
+    return refuse(fn, "temperature must be in 2^-60..2^60");
   const size_t a = dtype_size(dtype);
   if (!aligned(student, a) || !aligned(out_grad, a) || !aligned(teacher_logits, 4) ||
       !aligned(teacher_ids, 4) || !aligned(row_scale, 4) || !aligned(out_loss, 4))

@@ -83,7 +83,9 @@ def test_distill(lib):
                     (dict(e=0), b"n_classes"), (dict(e=(1 << 30) + 1), b"n_classes"), (dict(k=0), b"k must"),
                     (dict(k=257), b"k must"), (dict(t=0.0), b"temperature"), (dict(t=-1.0), b"temperature"),
                     (dict(t=float("nan")), b"temperature"), (dict(t=float("inf")), b"temperature"),
-                    (dict(t=1e-45), b"temperature"), (dict(student=ODD, dtype=1), b"misaligned"),
+                    (dict(t=1e-45), b"temperature"), (dict(t=3e-39), b"temperature"),
+                    (dict(t=2.0 ** -61), b"temperature"), (dict(t=2.0 ** 61), b"temperature"),
+                    (dict(t=3e38), b"temperature"), (dict(student=ODD, dtype=1), b"misaligned"),
                     (dict(grad=ctypes.c_void_p(4098)), b"misaligned"), (dict(scale=ODD), b"misaligned")):
         refused(lib, why, call(**kw))
 

@@ -335,6 +335,33 @@ def test_distill(torch, n, k, e, dtype, shift):
     assert torch.equal(ones, grad)
 
 
+@pytest.mark.parametrize("e", [40, 4096, 20001, 120001])
+def test_distill_temperatures_at_the_ends(torch, e):
+    """The lowest and the highest temperature that the call takes."""
+    import neural_radiance_field_b200 as nb
+    rng = np.random.default_rng(e)
+    n, k = 5, 6
+    s = np.stack([rng.permutation(e) for _ in range(n)]).astype(np.float32)
+    ids = np.stack([rng.permutation(e)[:k] for _ in range(n)]).astype(np.int32)
+    teacher = np.stack([rng.permutation(k) for _ in range(n)]).astype(np.float32)
+    loss, grad = torch.empty(n, device="cuda"), torch.empty(n, e, device="cuda")
+    T = 2.0 ** -60                                      # both distributions are one class: loss T (max s - s of the teacher's)
+    nb.nerf_distill_topk(_cuda(torch, s), _cuda(torch, teacher), _cuda(torch, ids), T, loss, grad)
+    want, rows = np.zeros((n, e)), np.arange(n)
+    want[rows, s.argmax(1)] += T
+    best = ids[rows, teacher.argmax(1)]
+    want[rows, best] -= T
+    assert np.array_equal(_np(grad), want)
+    gap = T * (s.max(1) - s[rows, best]).astype(np.float64)
+    _near(_np(loss), gap, 8 * U * gap, "loss")          # 1 / T, T T and powers of two are exact; the sums add zeros
+    T, one = 2.0 ** 60, np.ones(n)
+    nb.nerf_distill_topk(_cuda(torch, s), _cuda(torch, teacher), _cuda(torch, ids), T, loss, grad)
+    r_loss, r_grad = E.distill(s, teacher, ids, T)
+    b_loss, b_grad = _distill_bounds(s.astype(np.float64), teacher.astype(np.float64), ids, T, one, r_loss, r_grad, k)
+    _near(_np(loss), r_loss, b_loss, "loss")
+    _near(_np(grad), r_grad, b_grad + U * np.abs(r_grad), "grad")
+
+
 @pytest.mark.parametrize("e", [40, 4096, 20001])
 def test_distill_masks_and_extremes(torch, e):
     """Masks of the lowest value and of -inf, a kept class that the student rules out, NaN in rows that
