@@ -243,8 +243,11 @@ void run(const RowArgs& A) {
     rows_gather_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
                                                                 A.k, A.w, (T*)A.out, A.dw);
 }
-// pairs in chunks of two for k <= 2, of four for k <= 4, else of eight: an unused
-// place of a chunk costs its predicates, and a chunk's rows are all in flight at once
+// Pairs in chunks of two for k <= 2, of four for k <= 4, else of eight: an unused
+// place of a chunk costs its predicates and registers. 200,000 points of 256 bf16,
+// dispatch / combine / combine's backward: k 2 in chunks of two 49 / 46 / 78 us, of
+// four 49 / 54 / 84, of eight 51 / 120 / 86; k 4 of four 83 / 75 / 146, of eight
+// 83 / 131 / 148.
 template <bool SCATTER, typename T, int BYTES>
 void run_k(const RowArgs& A) {
   if (A.k <= 2) A.dw ? run<SCATTER, T, BYTES, 2, true>(A) : run<SCATTER, T, BYTES, 2, false>(A);
