@@ -24,12 +24,12 @@
 // would be split and written there (768 bytes a row forward) behind barriers, as
 // kilo_eval_kernel does for the renderer; at N = 32 that costs more than the
 // products. mma.sync runs at 0.9 TMAC/s an SM in tf32 (measured), 57 us for the
-// forward layers of 786,432 rows. With 786,432 rows over 4,096 cells (2,100 of
+// forward layers of 786,432 rows. With 786,432 rows over 4,096 cells (2,702 of
 // them with rows) the forward pass with its hidden layers takes 142 us (2.0 TB/s
-// of 287 MB, 0.31 of the copy rate; tensor pipe 42 % busy, issue slots 48 %, shared
-// memory 66 %), the weight gradient 195 us (tensor pipe 43 %, issue slots 54 %):
-// both are bound by each warp's chain of encoding, split and product at the 12 or
-// 16 warps that an SM's registers hold.
+// of 287 MB, 0.31 of the copy rate; tensor pipe 44 % busy, issue slots 50 %, shared
+// memory 52 %), the weight gradient 195 us (tensor pipe 45 %, issue slots 56 %,
+// shared memory 52 %): no unit is full, both are bound by each warp's chain of
+// encoding, split and product at the 16 or 12 warps that an SM's registers hold.
 #include "nerf_experts.cuh"
 
 namespace nerfb {

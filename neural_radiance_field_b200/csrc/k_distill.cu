@@ -19,7 +19,7 @@
 // before and after them go one by one.
 //
 // 65,536 rows of 4,096 bf16 with gradient: 207 us, 5.2 TB/s (0.81 of the measured
-// copy rate; two exponentials an element keep the XU pipe half busy). 777 rows of
+// copy rate; two exponentials an element keep the XU pipe 63 % busy). 777 rows of
 // 100,003 fp32: 152 us, 4.1 TB/s (0.64): 33 clusters of eight fit the GPCs, 264 of
 // 296 CTAs, and each row ends in a cluster barrier.
 #include <cooperative_groups.h>

@@ -14,15 +14,18 @@
 //            tile (16-bit counters, two experts a word), the counts are scanned
 //            over the warps (and, before the first tile's, the totals over the
 //            experts), and every warp walks its run in order, 32 pairs at a time.
-//            A match instruction finds which of the 32 share an expert (a ballot
-//            per bit of the id took longer), a pair's rank among them is the
-//            number of lower lanes, and the expert's counter advances by their
-//            number. Rows come out in pair order whatever the timing.
+//            Where experts are spread, every lane adds one to its expert's
+//            counter and reads it again: it met no one if it finds its own sum,
+//            and lanes that met are put in lane order. Where many meet, a match
+//            instruction finds who shares an expert (a ballot per bit of the id
+//            took longer) and one lane adds for all. Rows come out in pair order
+//            whatever the timing.
 // The launches overlap: place counts its first tile while columns still runs.
 //
-// 6.3 M pairs over 4,096 experts: 58 us, 1.3 TB/s of the 75 MB that the sort has
-// to read and write (0.20 of the copy rate). Place (about 40 us alone) is bound by
-// the match, 32 cycles of an SM for 32 pairs; count takes 10 us, columns 5.
+// 6.3 M pairs over 4,096 experts, eight neighbouring cells a point: 52 us, 1.4 TB/s of
+// the 75 MB that the sort has to read and write (0.22 of the copy rate); uniform
+// ids: 38 us. Count takes 10 us, columns 5; place is bound by its chains through
+// shared memory (counter, add, counter) at the 16 warps whose counters fit an SM.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
@@ -46,6 +49,13 @@ constexpr int ES_CHUNK = ES_T;
 constexpr int ES_MOST_CTAS = 148 * 2, ES_PER = (ES_MOST_CTAS + 15) / 16;
 constexpr int ES_WORDS = (EXPERT_MAX / 2 + ES_T - 1) / ES_T;   // counter words of a thread in the scan
 
+// Lanes that meet in a counter are put in order by a ballot per expert up to ES_FEW
+// of them, by a match above (6.3 M uniform pairs of 256 experts: 38 us, 56 by the
+// match alone); a warp goes over to matches where more than ES_MEET of its last 128
+// pairs met (one expert for all: 51 us, 61 to 66 by adds; uniform over 4,096: 38 us
+// by adds, 69 by matches; eight neighbouring cells a point: 52 either way). Both give
+// the same ranks.
+constexpr int ES_FEW = 4, ES_MEET = 16;
 struct SortPlan {
   int ctas;
   int64_t chunk;                             // pairs of a CTA, a multiple of ES_T
@@ -175,6 +185,7 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
   uint32_t* counts = reinterpret_cast<uint32_t*>(sm + n_experts);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   uint32_t* mine = counts + warp * words;
+  bool adds = true;
   const int64_t begin = blockIdx.x * chunk, end = min(pairs, begin + chunk);
   for (int64_t tile = begin; tile < end; tile += ES_TILE) {
     const int64_t left = min((int64_t)ES_TILE, end - tile);
@@ -259,29 +270,63 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
       ahead[q >> 2][q & 3] = r0 + 32 * q + lane < r1 ? __ldg(ids + r0 + 32 * q + lane) : -1;
     for (int64_t i0 = r0; i0 < r1; i0 += 128) {
       const int left = (int)min((int64_t)128, r1 - i0) - lane;   // this lane's pairs: 32 q < left
-      int id[4];
-      uint32_t peers[4];
+      int id[4], p[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         id[q] = (unsigned)ahead[0][q] < (unsigned)n_experts ? ahead[0][q] : -1;
         ahead[0][q] = ahead[1][q];
         ahead[1][q] = i0 + 256 + 32 * q + lane < r1 ? __ldg(ids + i0 + 256 + 32 * q + lane) : -1;
-        peers[q] = __match_any_sync(0xffffffffu, id[q]);
       }
+      int met = 0;                           // of the 128 pairs those with a later one of their expert in their 32
+      if (adds) {
+        int now[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {        // p: the counter before this lane's add; now: after all lanes'
+          const int at = id[q] < words ? id[q] : id[q] - words, shift = id[q] < words ? 0 : 16;
+          p[q] = 0, now[q] = 1;
+          if (id[q] >= 0) p[q] = (int)((atomicAdd(&mine[at], 1u << shift) >> shift) & 0xffffu);
+          __syncwarp();
+          if (id[q] >= 0) now[q] = (int)((reinterpret_cast<volatile uint32_t*>(mine)[at] >> shift) & 0xffffu);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {        // lanes that met in a counter: in lane order, not in that of their adds
+          uint32_t meet = __ballot_sync(0xffffffffu, now[q] != p[q] + 1);
+          met += __popc(meet);
+          if (__popc(meet) > ES_FEW) {
+            const uint32_t peers = __match_any_sync(0xffffffffu, id[q]);
+            if (id[q] >= 0) p[q] = now[q] - __popc(peers) + __popc(peers & lower);
+          } else {
+            while (meet) {
+              const int one = __shfl_sync(0xffffffffu, id[q], __ffs(meet) - 1);
+              const uint32_t peers = __ballot_sync(0xffffffffu, id[q] == one);
+              if (id[q] == one) p[q] = now[q] - __popc(peers) + __popc(peers & lower);
+              meet &= ~peers;
+            }
+          }
+        }
+      } else {
+        uint32_t peers[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) peers[q] = __match_any_sync(0xffffffffu, id[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = id[q] < words ? id[q] : id[q] - words, shift = id[q] < words ? 0 : 16;
+          p[q] = 0;
+          if (id[q] >= 0) p[q] = (int)((mine[at] >> shift) & 0xffffu) + __popc(peers[q] & lower);
+          met += __popc(__ballot_sync(0xffffffffu, id[q] >= 0 && (peers[q] & lower) != 0));
+          // one lane a peer group; the word's other expert may have one too, so the add is atomic
+          if (id[q] >= 0 && (peers[q] & lower) == 0) atomicAdd(&mine[at], (uint32_t)__popc(peers[q]) << shift);
+          __syncwarp();
+        }
+      }
+      adds = met <= ES_MEET;
       int32_t* dst = pos + i0 + lane;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        int32_t p = -1;
-        const int at = id[q] < words ? id[q] : id[q] - words, shift = id[q] < words ? 0 : 16;
-        if (id[q] >= 0) p = base[id[q]] + (int32_t)((mine[at] >> shift) & 0xffffu) + __popc(peers[q] & lower);
-        __syncwarp();
-        if (id[q] >= 0) {
-          // one lane a peer group; the word's other expert may have one too, so the add is atomic
-          if ((peers[q] & lower) == 0) atomicAdd(&mine[at], (uint32_t)__popc(peers[q]) << shift);
-          if (order) order[p] = (int32_t)i0 + lane + 32 * q;
-        }
-        if (32 * q < left) dst[32 * q] = p;
-        __syncwarp();
+        const int32_t row = id[q] >= 0 ? base[id[q]] + p[q] : -1;
+        if (id[q] >= 0 && order) order[row] = (int32_t)i0 + lane + 32 * q;
+        if (32 * q < left) dst[32 * q] = row;
       }
     }
     if (ALONE) return;

@@ -104,6 +104,23 @@ def test_sort_of_many_tiles(torch, n, k, e):
     assert torch.equal(pos.reshape(-1).long(), torch.where(key < e, place, -1))
 
 
+@pytest.mark.parametrize("e", [5, 200, 4095, 4096])
+@pytest.mark.parametrize("n", [777, 4096, 100003])
+def test_sort_of_ids_that_meet_more_and_less(torch, n, e):
+    """Runs of one expert, distinct ids, pairs of equal neighbours, ids that share a counter's word, dropped
+    ones between them: stretches of each, so that a warp meets all of them in turn."""
+    rng = np.random.default_rng([n, e])
+    i = np.arange(n)
+    kinds = np.stack([np.full(n, e - 1), i % e, (i // 2) % e, (i % 2) * ((e + 1) // 2) % e, (i // 16) % e, rng.integers(0, e, n),
+                      rng.integers(0, min(e, 3), n), np.where(i % 3 == 0, -1, i % e), np.full(n, -1)])
+    ids = kinds[rng.integers(0, len(kinds), n // 100 + 1)[i // 100], i].astype(np.int32).reshape(n, 1)
+    off, order, pos = _sorted(torch, _cuda(torch, ids), e)
+    r_off, r_order, r_pos = E.sort(ids, e)
+    assert np.array_equal(off.cpu().numpy(), r_off)
+    assert np.array_equal(pos.cpu().numpy(), r_pos)
+    assert np.array_equal(order.cpu().numpy()[:r_order.size], r_order)
+
+
 @pytest.mark.parametrize("n,k,e", [(60000, 2, 33), (60000, 2, 1000), (60000, 2, 4095)])
 def test_sorts_back_to_back_share_a_workspace(torch, n, k, e):
     """Launch follows launch with other ids and one workspace, expert counts that no 32 divide."""
