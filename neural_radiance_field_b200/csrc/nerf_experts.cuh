@@ -42,9 +42,9 @@ cudaError_t launch_cells_backward(const float* x, const float* d, int64_t n, con
 // before it reads a result of it, writes what it reads, or ends; and it takes those
 // results without const __restrict__, whose loads assume data that no one writes.
 template <typename K, typename... Args>
-cudaError_t launch_early(K kernel, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+cudaError_t launch_early(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

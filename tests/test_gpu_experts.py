@@ -507,6 +507,52 @@ def test_cells(torch, name):
     assert torch.equal(grad, again)
 
 
+def test_a_rows_value_does_not_depend_on_its_neighbours(torch):
+    """The same rows in one cell, and cut into cells of one to 70 rows that have the same weights: the same bits."""
+    import neural_radiance_field_b200 as nb
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    counts = [1, 2, 7, 8, 9, 0, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 70, 127, 128, 129, 160, 161]
+    n = sum(counts)
+    x, d, w = rnd(n, 3), rnd(n, 3), rnd(1, 3317) * 0.1
+    outs = []
+    for off in ([0, n], np.concatenate([[0], np.cumsum(counts)])):
+        off = _cuda(torch, np.asarray(off, dtype=np.int32))
+        raw, hidden = torch.full((n, 4), 7.0, device="cuda"), torch.full((n, 64), 7.0, device="cuda")
+        nb.nerf_cells_forward(x, d, off, w.expand(off.numel() - 1, -1).contiguous(), raw, hidden)
+        outs.append((raw, hidden))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("cells", [1, 3, 64, 200, 591])
+def test_cell_gradients_of_few_cells(torch, cells):
+    """Few cells have their parts summed in slices: the bits that they get among 1,000 cells of which the rest is
+    empty, and biases that are the plain sums of d_raw. Of the magnitudes' sum: 4 U for a value as two tf32 numbers
+    (the lower one's own rounding, 2^-11 of 2^-11), 6 x 16 U for a tile's six matrix instructions (eight truncated
+    terms each, 2 U a term), then at most one rounded addition a row."""
+    import neural_radiance_field_b200 as nb
+    gen = torch.Generator(device="cuda").manual_seed(cells)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    n = 30000
+    x, d, w, d_raw = rnd(n, 3), rnd(n, 3), rnd(1000, 3317) * 0.1, rnd(n, 4)
+    off = np.concatenate([[0], np.sort(np.random.default_rng(cells).integers(0, n + 1, cells - 1)), [n]])
+    grads = []
+    for many in (cells, 1000):
+        o = _cuda(torch, np.concatenate([off, np.full(many - cells, n)]).astype(np.int32))
+        raw, hidden = torch.empty(n, 4, device="cuda"), torch.empty(n, 64, device="cuda")
+        nb.nerf_cells_forward(x, d, o, w[:many], raw, hidden)
+        grads.append(torch.full((many, 3317), float("nan"), device="cuda"))
+        work = torch.empty(nb.nerf_cells_backward_workspace(n, many), device="cuda", dtype=torch.uint8)
+        nb.nerf_cells_backward(x, d, o, w[:many], hidden, d_raw, grads[-1], work)
+    assert torch.equal(grads[0], grads[1][:cells]) and grads[1][cells:].eq(0).all()
+    got, terms = _np(grads[0]), _np(d_raw)
+    for c in range(cells):
+        rows = terms[off[c]:off[c + 1]]
+        bound = (len(rows) + 100) * U * np.abs(rows).sum(0)
+        _near(got[c, 3314:3317], rows[:, :3].sum(0), bound[:3], "color biases")
+        _near(got[c, 3136:3137], rows[:, 3:].sum(0), bound[3:], "sigma bias")
+
+
 def test_cell_gradients_back_to_back_share_a_workspace(torch):
     """Launch follows launch with other rows per cell and one workspace: every result is that of the call alone."""
     import neural_radiance_field_b200 as nb
