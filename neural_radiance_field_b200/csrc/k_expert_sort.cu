@@ -315,6 +315,7 @@ sort_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int64_t chunk,
           p[q] = 0;
           if (id[q] >= 0) p[q] = (int)((mine[at] >> shift) & 0xffffu) + __popc(peers[q] & lower);
           met += __popc(__ballot_sync(0xffffffffu, id[q] >= 0 && (peers[q] & lower) != 0));
+          __syncwarp();                      // every lane has read its counter before one lane adds to it
           // one lane a peer group; the word's other expert may have one too, so the add is atomic
           if (id[q] >= 0 && (peers[q] & lower) == 0) atomicAdd(&mine[at], (uint32_t)__popc(peers[q]) << shift);
           __syncwarp();

@@ -141,6 +141,21 @@ def test_sorts_back_to_back_share_a_workspace(torch, n, k, e):
             np.testing.assert_array_equal(got_pos.cpu().numpy(), pos)
 
 
+@pytest.mark.parametrize("e", [2, 7, 1000, 4096])
+@pytest.mark.parametrize("n", [3000, 200003])
+def test_sort_of_two_experts_that_share_a_counter_word(torch, n, e):
+    """Every 32 pairs meet in one word of two counters: what the lanes of one expert read of it comes before
+    what a lane of either adds to it."""
+    words = (e + 1) // 2
+    low = np.random.default_rng([n, e]).integers(0, e - words, n // 500 + 1)[np.arange(n) // 500]
+    ids = (low + words * np.random.default_rng([e, n]).integers(0, 2, n)).astype(np.int32).reshape(n, 1)
+    off, order, pos = _sorted(torch, _cuda(torch, ids), e)
+    r_off, r_order, r_pos = E.sort(ids, e)
+    assert np.array_equal(off.cpu().numpy(), r_off)
+    assert np.array_equal(pos.cpu().numpy(), r_pos)
+    assert np.array_equal(order.cpu().numpy(), r_order)
+
+
 def test_sort_agrees_with_the_cell_router(torch):
     """One cell per point: the same counts and cells as nerf_test_route_cells."""
     import neural_radiance_field_b200 as nb
