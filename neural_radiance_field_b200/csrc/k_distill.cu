@@ -80,12 +80,14 @@ __device__ __forceinline__ float2 warp_join(float2 v, float c) {
   return make_float2(m, warp_fold(z, [](float a, float b) { return a + b; }));
 }
 // The whole CTA's (maximum, sum); `red` holds two sets used in turn, so that one
-// barrier a call is enough.
-template <int NT>
+// barrier a call is enough. It is barrier BAR of the CTA by its number: a kernel whose
+// warps call from two places meets there all the same, which __syncthreads, a call of
+// all threads from one place, does not promise.
+template <int NT, int BAR>
 __device__ __forceinline__ float2 cta_join(float2 v, float c, float2* red) {
   v = warp_join(v, c);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
+  asm volatile("barrier.sync %0, %1;" ::"n"(BAR), "n"(NT) : "memory");
   constexpr int W = NT / 32;
   return warp_join((threadIdx.x & 31) < W ? red[threadIdx.x & 31] : make_float2(-INFINITY, 0.0f), c);
 }
@@ -202,11 +204,12 @@ __device__ __forceinline__ void kept_gradients_warp(const Teacher& R, T* g, floa
 // A CTA's (maximum, sum) joined over its cluster: every CTA writes its own to all,
 // and one cluster barrier later each has them all at hand. `stat` is one of two
 // sets used in turn: a set is written again only after the next row's barrier,
-// which no CTA passes before all have read it.
+// which no CTA passes before all have read it. The barrier is the form that warps may
+// reach from different places.
 __device__ __forceinline__ float2 cluster_join(float2 v, float c, float2* stat, int rank, int C) {
   cg::cluster_group cluster = cg::this_cluster();
   if ((int)threadIdx.x < C) cluster.map_shared_rank(stat, threadIdx.x)[rank] = v;
-  cluster.sync();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   const int lane = threadIdx.x & 31;
   return warp_join(lane < C ? stat[lane] : make_float2(-INFINITY, 0.0f), c);
 }
@@ -394,7 +397,7 @@ distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
       teacher_solve(A, i, R, probs, ids);
       if (t == DS_M) some_s[turn] = R.some;
       __syncwarp();
-      float2 all = cta_join<DS_T>(make_float2(-INFINITY, 0.0f), c, red[turn]);
+      float2 all = cta_join<DS_T, 2>(make_float2(-INFINITY, 0.0f), c, red[turn]);
       if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
       const Teacher now = R;
       R = teacher_load<T>(A, i + step);
@@ -440,7 +443,7 @@ distill_stage_kernel(DistillArgs A, int C, int stage_vecs) {
       F2 zp[2] = {F2::of(exp2_fast((one - shift) * c), 0.0f), F2::of(0.0f, 0.0f)};
 #pragma unroll 2
       for (int q = t; q < nv; q += DS_M) pass_sum(V::of(v[q]), F2::of(-shift, -shift), c2, zp);
-      float2 all = cta_join<DS_T>(make_float2(top, whole_sum(zp)), c, red[turn]);
+      float2 all = cta_join<DS_T, 2>(make_float2(top, whole_sum(zp)), c, red[turn]);
       if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
       const float m = all.x, aiz = a / all.y;
       const bool some = some_s[turn];
@@ -514,7 +517,7 @@ distill_wide_kernel(DistillArgs A, int C) {
 #pragma unroll
           for (int e = 0; e < V::N; ++e) z += exp2_fast((v[u].get(e) - shift) * c);
     }
-    float2 all = cta_join<DW_T>(make_float2(m, z), c, red[turn]);
+    float2 all = cta_join<DW_T, 0>(make_float2(m, z), c, red[turn]);
     if (C > 1) all = cluster_join(all, c, stat[turn], rank, C);
     m = all.x;
     z = all.y;

@@ -420,6 +420,24 @@ def test_distill_masks_and_extremes(torch, e):
     assert abs(loss[4].item() - want) <= 20 * U * (np.log(e) + 2) + (e / 32 + 16) * U
 
 
+@pytest.mark.parametrize("e,dtype", [(5003, "fp32"), (20001, "fp32"), (60000, "bf16"), (100003, "fp32")])
+def test_distill_rows_of_one_call_are_those_of_calls_of_their_own(torch, e, dtype):
+    """A CTA, and clusters of two, four and eight, that take several rows one after another: each row's loss and
+    gradient are the bits of a call on it alone."""
+    import neural_radiance_field_b200 as nb
+    gen = torch.Generator(device="cuda").manual_seed(e)
+    n, k, t = 700, 5, _t(torch, dtype)
+    s = torch.randn(n, e, device="cuda", generator=gen).to(t)
+    tl, ti = torch.randn(n, k, device="cuda", generator=gen), torch.randint(0, e, (n, k), device="cuda", generator=gen, dtype=torch.int32)
+    ti[::7] = -1
+    loss, grad = torch.full((n,), 7.0, device="cuda"), torch.full((n, e), 7.0, device="cuda", dtype=t)
+    nb.nerf_distill_topk(s, tl, ti, 2.0, loss, grad)
+    for i in (0, 1, 6, 7, 36, 37, 147, 148, 295, 296, 297, 443, 592, 699):
+        one, g = torch.empty(1, device="cuda"), torch.empty(n, e, device="cuda", dtype=t)[i:i + 1]   # aligned like row i
+        nb.nerf_distill_topk(s[i:i + 1], tl[i:i + 1], ti[i:i + 1], 2.0, one, g)
+        assert torch.equal(one[0], loss[i]) and torch.equal(g[0], grad[i])
+
+
 # ------------------------------------------------------------------ per-cell networks
 
 C3 = 1.25 * 2.0 ** -20      # a product of two operands split in three: lo parts read at 2^-10, lo * lo dropped
