@@ -170,11 +170,21 @@ def _rows_dtype(name, t):
     return t.dtype, code
 
 
+def _size(name, v, bits=32):
+    """A size as the C ABI's signed integer of `bits` bits, which ctypes would cut to them unasked."""
+    v = int(v)
+    if not -(1 << bits - 1) <= v < 1 << bits - 1:
+        raise ValueError(f"{name}: {v} does not fit {bits} bits")
+    return v
+
+
 def _shape2(name, t):
-    """Sizes of a tensor of two dimensions."""
+    """Sizes of a tensor of two dimensions, the second (a C int) below 2^31."""
     s = getattr(t, "shape", ())
     if len(s) != 2:
         raise ValueError(f"{name}: expected a tensor of 2 dimensions")
+    if s[1] >= 1 << 31:
+        raise ValueError(f"{name}: {s[1]} columns do not fit 32 bits")
     return s
 
 
@@ -198,7 +208,8 @@ def _call(fn, *args, stream, dev):
 def nerf_expert_sort_workspace(n, k, n_experts):
     """Bytes of workspace that nerf_expert_sort needs."""
     b = ctypes.c_int64()
-    _capi.check(_capi.lib().nerf_expert_sort_workspace(int(n), int(k), int(n_experts), ctypes.byref(b)))
+    _capi.check(_capi.lib().nerf_expert_sort_workspace(_size("n", n, 64), _size("k", k), _size("n_experts", n_experts),
+                                                        ctypes.byref(b)))
     return b.value
 
 
@@ -207,7 +218,8 @@ def nerf_expert_sort(ids, n_experts, out_offset, out_order, out_pos, workspace, 
     or None; workspace: any tensor of at least nerf_expert_sort_workspace bytes."""
     import torch
     n, k = _shape2("ids", ids)
-    i32, dev, e = torch.int32, _current("ids", ids), int(n_experts)
+    e = _size("n_experts", n_experts)
+    i32, dev = torch.int32, _current("ids", ids)
     _call("nerf_expert_sort", _arg("ids", ids, i32, (n, k), dev), n, k, e,
           _arg("out_offset", out_offset, i32, (e + 1,), dev), _opt("out_order", out_order, i32, (n * k,), dev),
           _arg("out_pos", out_pos, i32, (n, k), dev), *_work(workspace, dev), stream=stream, dev=dev)
@@ -275,7 +287,7 @@ def nerf_distill_topk(student, teacher_logits, teacher_ids, temperature, out_los
 def nerf_cells_forward(x, d, offset, cell_w, out_raw, out_hidden=None, stream=None):
     """Per-cell networks on rows sorted by cell: out_raw [n, 4], out_hidden [n, 64] or None."""
     import torch
-    n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
+    n, e = _shape2("x", x)[0], _size("n_cells", _shape2("cell_w", cell_w)[0])
     f32, dev = torch.float32, _current("x", x)
     _call("nerf_cells_forward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
           _arg("offset", offset, torch.int32, (e + 1,), dev), e,
@@ -286,14 +298,14 @@ def nerf_cells_forward(x, d, offset, cell_w, out_raw, out_hidden=None, stream=No
 def nerf_cells_backward_workspace(n_rows, n_cells):
     """Bytes of workspace that nerf_cells_backward needs."""
     b = ctypes.c_int64()
-    _capi.check(_capi.lib().nerf_cells_backward_workspace(int(n_rows), int(n_cells), ctypes.byref(b)))
+    _capi.check(_capi.lib().nerf_cells_backward_workspace(_size("n_rows", n_rows, 64), _size("n_cells", n_cells), ctypes.byref(b)))
     return b.value
 
 
 def nerf_cells_backward(x, d, offset, cell_w, hidden, d_raw, grad_cell_w, workspace, stream=None):
     """Weight gradient of nerf_cells_forward (overwritten), from its hidden layers."""
     import torch
-    n, e = _shape2("x", x)[0], _shape2("cell_w", cell_w)[0]
+    n, e = _shape2("x", x)[0], _size("n_cells", _shape2("cell_w", cell_w)[0])
     f32, dev = torch.float32, _current("x", x)
     _call("nerf_cells_backward", _arg("x", x, f32, (n, 3), dev), _arg("d", d, f32, (n, 3), dev), n,
           _arg("offset", offset, torch.int32, (e + 1,), dev), e,

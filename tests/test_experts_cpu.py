@@ -128,3 +128,29 @@ def test_binding_refuses_what_the_library_cannot_see():
         nb.nerf_distill_topk(x, torch.zeros(4), torch.zeros(4, dtype=i32), 1.0, torch.zeros(4))
     with pytest.raises(ValueError, match="2 dimensions"):
         nb.nerf_cells_forward(x, x, pos, torch.zeros(3317), x)
+
+
+def test_binding_refuses_sizes_that_would_be_cut_to_32_bits():
+    """2^32 + 8 is not 8: tensors without memory, so that the refusal comes before anything else."""
+    import torch
+    import neural_radiance_field_b200 as nb
+    big, i32 = (1 << 32) + 8, torch.int32
+    meta = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="meta")  # noqa: E731
+    wide, x = meta(4, big), meta(4, 8)
+    ids, pos = meta(4, big, t=i32), meta(4, 2, t=i32)
+    calls = [lambda: nb.nerf_expert_sort_workspace(4, 2, big), lambda: nb.nerf_expert_sort_workspace(4, big, 8),
+             lambda: nb.nerf_expert_sort_workspace((1 << 64) + 4, 2, 8), lambda: nb.nerf_cells_backward_workspace(8, big),
+             lambda: nb.nerf_cells_backward_workspace((1 << 64) + 8, 8),
+             lambda: nb.nerf_expert_sort(pos, big, meta(big + 1, t=i32), None, pos, x),
+             lambda: nb.nerf_expert_sort(ids, 8, meta(9, t=i32), None, ids, x),
+             lambda: nb.nerf_expert_dispatch(wide, pos, wide), lambda: nb.nerf_expert_dispatch(x, ids, x),
+             lambda: nb.nerf_expert_dispatch_backward(wide, None, pos, wide), lambda: nb.nerf_expert_dispatch_backward(x, x, ids, x),
+             lambda: nb.nerf_expert_combine(wide, pos, wide), lambda: nb.nerf_expert_combine(x, ids, x),
+             lambda: nb.nerf_expert_combine_backward(wide, None, pos, wide), lambda: nb.nerf_expert_combine_backward(x, x, ids, x),
+             lambda: nb.nerf_distill_topk(wide, x, pos, 1.0, x), lambda: nb.nerf_distill_topk(x, x, ids, 1.0, x),
+             lambda: nb.nerf_cells_forward(x, x, pos, meta(big, 3317), x),
+             lambda: nb.nerf_cells_backward(x, x, pos, meta(big, 3317), x, x, x, x)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="fit (32|64) bits"):
+            call()
+            pytest.fail(f"call {i} was not refused")
