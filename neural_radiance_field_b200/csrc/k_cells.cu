@@ -47,10 +47,17 @@ __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // v = hi + lo: hi the nearest tf32 (10 stored bits, ties away from zero), lo exact;
-// the tensor core reads lo at tf32 precision.
+// the tensor core reads lo at tf32 precision. An infinity or NaN has a NaN as one of
+// the two, so what is computed from it is NaN.
 __device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(__fsub_rn(v, __uint_as_float(hi)));
+}
+// max(v, 0) that keeps a NaN: a row or cell that is no longer finite shows it
+__device__ __forceinline__ float relu(float v) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(v));
+  return y;
 }
 // sin and cos of pi v: v = n / 2 + r exactly, |r| <= 1/4, and two polynomials in
 // r^2 whose coefficients were fitted to sin(pi r) / r and cos(pi r) on that
@@ -289,7 +296,7 @@ __device__ __forceinline__ void forward_rows(const CellsForwardShared& S, const 
       h2[m][j][0] = h2[m][j][2] = b.x;
       h2[m][j][1] = h2[m][j][3] = b.y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[m][j][i] = fmaxf(h[m][j][i], 0.0f);
+      for (int i = 0; i < 4; ++i) h[m][j][i] = relu(h[m][j][i]);
     }
   }
   if (hidden) store_hidden<R, M>(hidden + row0 * 64, h, g, t, rows);
@@ -309,7 +316,7 @@ __device__ __forceinline__ void forward_rows(const CellsForwardShared& S, const 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h2[m][j][i] = fmaxf(h2[m][j][i], 0.0f);
+      for (int i = 0; i < 4; ++i) h2[m][j][i] = relu(h2[m][j][i]);
   if (hidden) store_hidden<R, M>(hidden + row0 * 64 + 32, h2, g, t, rows);
   // the heads on the FMA pipe, which the tensor products leave idle: each lane
   // its eight features of h2 and its share of gamma(d), for R rows

@@ -631,6 +631,76 @@ def test_cells_far_positions(torch):
     assert (np.abs(_np(hid) - r_hid) <= 33 * e).all()
 
 
+def _cells_once(torch, x, d, off, w):
+    import neural_radiance_field_b200 as nb
+    raw, hid = torch.full((len(x), 4), 7.0, device="cuda"), torch.full((len(x), 64), 7.0, device="cuda")
+    nb.nerf_cells_forward(_cuda(torch, x), _cuda(torch, d), _cuda(torch, off), _cuda(torch, w), raw, hid)
+    return raw, hid
+
+
+@pytest.mark.parametrize("rows", [5, 40, 200])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_cells_that_are_not_finite_show_it(torch, rows, bad):
+    """NaN or infinity in one row's position: NaN in that row's hidden layers and outputs; in its direction: in its
+    colours; in one weight of one cell: in what that cell computes from it. Every other row keeps its bits."""
+    rng, off, x, d, w = _cells_case(torch, rows, [rows, rows + 3, 0, rows])
+    raw, hid = _cells_once(torch, x, d, off, w)
+    assert torch.isfinite(raw).all() and torch.isfinite(hid).all()
+    same = lambda a, b, r: torch.equal(a[r], b[r])  # noqa: E731
+    for r in (0, rows - 1, rows + 2, 2 * rows + 3):
+        others = torch.arange(len(x), device="cuda") != r
+        for c in range(3):
+            x2 = x.copy()
+            x2[r, c] = bad
+            raw2, hid2 = _cells_once(torch, x2, d, off, w)
+            assert torch.isnan(hid2[r]).all() and torch.isnan(raw2[r]).all()
+            assert same(raw, raw2, others) and same(hid, hid2, others)
+            d2 = d.copy()
+            d2[r, c] = bad
+            raw2, hid2 = _cells_once(torch, x, d2, off, w)
+            assert torch.isnan(raw2[r, :3]).all() and raw2[r, 3] == raw[r, 3] and torch.equal(hid, hid2) and same(raw, raw2, others)
+    mine = torch.zeros(len(x), device="cuda", dtype=torch.bool)
+    mine[rows:2 * rows + 3] = True
+    f = 9                                                # the feature whose weight is not finite
+    for at, layer in ((f * 63 + 20, 1), (2016 + f, 1), (2048 + f * 32 + 3, 2), (3072 + f, 2)):   # W1, b1, W2, b2
+        w2 = w.copy()
+        w2[1, at] = bad
+        raw2, hid2 = _cells_once(torch, x, d, off, w2)
+        assert same(raw, raw2, ~mine) and same(hid, hid2, ~mine)
+        if at in (2016 + f, 3072 + f) and bad == -np.inf:    # a bias of -inf turns its feature off
+            off1 = hid2[mine, 32 * (layer - 1) + f]
+            assert off1.eq(0).all()
+            continue
+        hit = hid2[mine]
+        assert (~torch.isfinite(hit[:, 32 * (layer - 1) + f])).all() and (~torch.isfinite(raw2[mine])).all()
+        if layer == 2:
+            assert same(hid[:, :32], hid2[:, :32], mine)
+
+
+@pytest.mark.parametrize("rows", [5, 200])
+def test_cell_gradients_that_are_not_finite_show_it(torch, rows):
+    """A row with a NaN position: NaN in the gradients of its cell's weights on gamma(x) and on the hidden layers; the
+    bits of every other cell's gradient stay."""
+    import neural_radiance_field_b200 as nb
+    rng, off, x, d, w = _cells_case(torch, rows, [rows, rows + 3, 0, rows])
+    g = _cuda(torch, rng.normal(size=(len(x), 4)).astype(np.float32))
+    work = torch.empty(nb.nerf_cells_backward_workspace(len(x), 4), device="cuda", dtype=torch.uint8)
+    grads = []
+    for bad in (False, True):
+        if bad:
+            x[rows + 1, 2] = np.nan
+        _, hid = _cells_once(torch, x, d, off, w)
+        grads.append(torch.full((4, E.N_CELL), 7.0, device="cuda"))
+        nb.nerf_cells_backward(_cuda(torch, x), _cuda(torch, d), _cuda(torch, off), _cuda(torch, w), hid, g, grads[-1], work)
+    assert torch.isfinite(grads[0]).all()
+    assert all(torch.equal(grads[0][c], grads[1][c]) for c in (0, 2, 3))
+    w1, _, w2, _, ws, _, wc, _ = torch.split(grads[1][1], [2016, 32, 1024, 32, 32, 1, 177, 3])
+    z = w1.view(32, 63)                                  # coordinate 2 and its angles; the others' factors stay finite
+    cols = [2, *range(23, 33), *range(53, 63)]
+    assert torch.isnan(z[:, cols]).all()
+    assert torch.isnan(w2).all() and torch.isnan(ws).all() and torch.isnan(wc.view(3, 59)[:, :32]).all()
+
+
 def test_cells_agree_with_the_renderers_network(torch):
     """sigma and rgb of one KiloNeRF frame: each ray marched by hand through nerf_test_march's live samples,
     nerf_expert_sort and nerf_cells_forward composites to nerf_render's colour."""
