@@ -468,15 +468,16 @@ NERF_API nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n
                                        float* out_loss, void* out_grad, void* stream);
 
 /* The KiloNeRF cell networks (nerf_params.cell_w) on rows sorted by cell:
- * x, d [n_rows][3] fp32 (d normalised inside), offset [n_cells + 1] int32 as
- * nerf_expert_sort writes it (rows offset[c] .. offset[c+1]-1 belong to cell c),
- * cell_w [n_cells][3317]. out_raw [n_rows][4] = (r, g, b, sigma) before their
- * activations; out_hidden (may be NULL) [n_rows][64]: the two hidden layers
- * after ReLU, for the backward pass. Rows from offset[n_cells] on are left as
- * they were. fp32 accuracy (tensor-core products split in three). n_rows <= 2^30.
- * A NaN stays in all that is computed from it, hidden layers included, and in no
- * other row or cell; an infinite factor of a product, and a position of 2^119 or
- * more (its angles overflow), count as NaN. */
+ * x, d [n_rows][3] fp32 (d, of any length but 0, normalised inside), offset
+ * [n_cells + 1] int32 as nerf_expert_sort writes it (rows offset[c] ..
+ * offset[c+1]-1 belong to cell c), cell_w [n_cells][3317]. out_raw [n_rows][4] =
+ * (r, g, b, sigma) before their activations; out_hidden (may be NULL)
+ * [n_rows][64]: the two hidden layers after ReLU, for the backward pass. Rows
+ * from offset[n_cells] on are left as they were. fp32 accuracy (tensor-core
+ * products split in three). n_rows <= 2^30. A NaN stays in all that is computed
+ * from it, hidden layers included, and in no other row or cell; an infinite
+ * factor of a product, and a position of 2^119 or more (its angles overflow),
+ * count as NaN. */
 NERF_API nerf_status nerf_cells_forward(const float* x, const float* d, int64_t n_rows,
                                         const int32_t* offset, int n_cells, const float* cell_w,
                                         float* out_raw, float* out_hidden, void* stream);

@@ -76,8 +76,16 @@ __device__ __forceinline__ void sincos_pi(float v, float* s, float* c) {
   *s = __uint_as_float(__float_as_uint(p) ^ ((n << 30) & 0x80000000u));
   *c = __uint_as_float(__float_as_uint(o) ^ (((n + 1) << 30) & 0x80000000u));
 }
-// the unit direction: each coordinate divided by the rounded norm
+// The unit direction: each coordinate divided by the rounded norm, after a scale by
+// the power of two that brings the largest coordinate's exponent to 0 (at the ends of
+// the range it lands within 2^-22 .. 4), so that no square overflows or loses its bits. The scale
+// is exact and changes no bit of a direction whose squares did neither.
 __device__ __forceinline__ void unit3(float* d) {
+  const uint32_t most = __float_as_uint(fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fabsf(d[2]))) & 0x7f800000u;
+  const float scale = __uint_as_float(0x7f000000u - min(most, 0x7e800000u));
+  d[0] *= scale;
+  d[1] *= scale;
+  d[2] *= scale;
   const float len = sqrtf(fmaf(d[0], d[0], fmaf(d[1], d[1], d[2] * d[2])));
   d[0] /= len;
   d[1] /= len;

@@ -701,6 +701,42 @@ def test_cell_gradients_that_are_not_finite_show_it(torch, rows):
     assert torch.isnan(w2).all() and torch.isnan(ws).all() and torch.isnan(wc.view(3, 59)[:, :32]).all()
 
 
+def test_cells_directions_of_every_length(torch):
+    """Directions from the smallest floats to the largest: the colours are the unit direction's, whose coordinates are
+    within 3.5u each, through gamma(d) and the head (the bounds of test_cells; the layers below are the same)."""
+    length = np.array([2.0 ** e for e in (-148, -140, -130, -126, -100, -75, -64, -63, -40, 0, 40, 62, 63, 64, 90, 120, 126)])
+    base = np.random.default_rng(4).normal(size=(len(length), 3))
+    base /= np.abs(base).max(1, keepdims=True)
+    d = (base * length[:, None]).astype(np.float32)
+    d = np.concatenate([d, np.float32([[3.4e38, -3.4e38, 3.4e38], [0, 0, 1e-45], [0, -2.0 ** 127, 0], [1e-20, 1e-20, 0], [1e18, 0, 1e18],
+                                       [1e30, 1e-30, 1e10], [-1e-42, 1e-44, 1.0]])])
+    n = len(d)
+    x = np.tile(np.float32([[0.3, -0.2, 0.9]]), (n, 1))
+    w, off = kilonerf_weights(9, n_cells=1), np.array([0, n], np.int32)
+    raw, hid = _cells_once(torch, x, d, off, w)
+    assert (hid == hid[0]).all() and (raw[:, 3] == raw[0, 3]).all()
+    _, _, _, _, _, _, wc, bc = (np.abs(v) for v in E.cell_parts(w[0]))
+    _, pd = E.encodings(x, d)
+    _, ed = _encoding_errors(x, d.astype(np.float64))
+    h2 = _np(hid)[:, 32:]                                # the head's other inputs, as the call wrote them
+    _, _, _, _, _, _, swc, sbc = E.cell_parts(w[0])
+    ref = np.concatenate([h2, pd], axis=1) @ swc.T + sbc
+    mag = np.concatenate([h2, np.abs(pd) + ed], axis=1) @ wc.T + bc
+    _near(_np(raw)[:, :3], ref, 1.01 * (ed @ wc[:, 32:].T + 62 * U * mag), "colours")
+    # and in the weight gradient, of which a row alone in its cell with d_raw = (1, 0, 0, 0) shows gamma(d): a product
+    # with 1 of two tf32 parts (the lower one cut, 2^-21), two truncated sums with zeros (2U each), one rounded. Of a
+    # coordinate below the normal range (one is 1e-60, which is 0 in fp32) the parts' steps are 2^-136 or the parts 0:
+    # 2^-126
+    import neural_radiance_field_b200 as nb
+    d_raw = torch.zeros(n, 4, device="cuda")
+    d_raw[:, 0] = 1
+    grad = torch.full((n, E.N_CELL), 7.0, device="cuda")
+    work = torch.empty(nb.nerf_cells_backward_workspace(n, n), device="cuda", dtype=torch.uint8)
+    nb.nerf_cells_backward(_cuda(torch, x), _cuda(torch, d), torch.arange(n + 1, device="cuda", dtype=torch.int32),
+                           _cuda(torch, np.repeat(w, n, axis=0)), hid, d_raw, grad, work)
+    _near(_np(grad)[:, 3137 + 32:3137 + 59], pd, 1.01 * (ed + (2.0 ** -21 + 5 * U) * (np.abs(pd) + ed)) + 2.0 ** -126, "gradient of the head")
+
+
 def test_cells_agree_with_the_renderers_network(torch):
     """sigma and rgb of one KiloNeRF frame: each ray marched by hand through nerf_test_march's live samples,
     nerf_expert_sort and nerf_cells_forward composites to nerf_render's colour."""
