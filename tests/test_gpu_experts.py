@@ -737,6 +737,34 @@ def test_cells_directions_of_every_length(torch):
     _near(_np(grad)[:, 3137 + 32:3137 + 59], pd, 1.01 * (ed + (2.0 ** -21 + 5 * U) * (np.abs(pd) + ed)) + 2.0 ** -126, "gradient of the head")
 
 
+def test_cells_encodings_of_far_positions(torch):
+    """Each column of gamma(x), read out by cells whose first layer is one of its columns and its negative, with the
+    sines of angles that are exact: k pi v with 2^k v taken modulo 2 before anything is rounded. The product with 1
+    reads the value as its two tf32 parts, the lower one cut at 2^-10 of its 2^-11; its sum with zeros truncates
+    twice, 2U each."""
+    x = np.float32([[0.3, -1.4999, 0.7], [100.25, -2999.7, 0.1], [2.0 ** 23, 3.0, -2.0 ** 24], [-1023.5, 511.75, 4095.0625],
+                    [0.0, -0.0, 1e-30], [8388607.5, -8388608.0, 16777215.0], [65535.996, -32767.502, 1048575.94],
+                    [2.0 ** 30, -2.0 ** 60, 2.0 ** 100], [12345.678, -0.5, 33554434.0]])
+    n, cells = len(x), 4
+    w = np.zeros((cells, E.N_CELL), np.float32)
+    for c in range(cells):
+        w1 = w[c, :2016].reshape(32, 63)
+        for j in range(16):
+            if 16 * c + j < 63:
+                w1[j, 16 * c + j], w1[16 + j, 16 * c + j] = 1.0, -1.0
+    d = np.tile(np.float32([[0, 0, 1]]), (n * cells, 1))
+    off = (n * np.arange(cells + 1)).astype(np.int32)
+    # far columns of x itself are left out of their rows' sums only by a weight of 0; they are finite
+    _, hid = _cells_once(torch, np.tile(x, (cells, 1)), d, off, w)
+    h = _np(hid)[:, :32].reshape(cells, n, 2, 16)
+    assert ((h[:, :, 0] == 0) | (h[:, :, 1] == 0)).all()
+    got = (h[:, :, 0] - h[:, :, 1]).transpose(1, 0, 2).reshape(n, 64)[:, :63]
+    half = np.fmod(x.astype(np.float64)[:, :, None] * 2.0 ** np.arange(10), 2.0).reshape(n, 30)
+    ref = np.concatenate([x, np.sin(np.pi * half), np.cos(np.pi * half)], axis=1)
+    ex = _encoding_errors(x, np.ones((n, 3)))[0]
+    _near(got, ref, 1.01 * (ex + (2.0 ** -21 + 4 * U) * np.abs(ref)) + 4e-16, "gamma(x)")
+
+
 def test_cells_agree_with_the_renderers_network(torch):
     """sigma and rgb of one KiloNeRF frame: each ray marched by hand through nerf_test_march's live samples,
     nerf_expert_sort and nerf_cells_forward composites to nerf_render's colour."""
