@@ -476,7 +476,7 @@ NERF_API nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n
  * from offset[n_cells] on are left as they were. fp32 accuracy (tensor-core
  * products split in three). n_rows <= 2^30. A NaN stays in all that is computed
  * from it, hidden layers included, and in no other row or cell; an infinite
- * factor of a product, and a position of 2^119 or more (its angles overflow),
+ * factor of a product, and a position of 2^120 or more (its angles overflow),
  * count as NaN. */
 NERF_API nerf_status nerf_cells_forward(const float* x, const float* d, int64_t n_rows,
                                         const int32_t* offset, int n_cells, const float* cell_w,

@@ -155,17 +155,20 @@ __device__ __forceinline__ void teacher_solve(const DistillArgs& A, int64_t i, T
   R.plogp = warp_sum(l);
 }
 
-// The row's loss, by the warp that has its teacher.
+// The row's loss, by the warp that has its teacher:
+//   T^2 (sum_j p_j log p_j + log Z) - T sum_j p_j (s_j - m),
+// the p_j summing to 1. The gaps s - m meet T, not T^2 / T: a class that the teacher
+// keeps and the student masks with its type's lowest value has a finite loss.
 template <typename T>
 __device__ __forceinline__ void write_loss(const DistillArgs& A, int64_t i, const T* s, float m, float z,
                                            const float* probs, const int32_t* ids, const Teacher& R) {
   const int lane = threadIdx.x & 31;
-  const float inv_t = 1.0f / A.temperature, log_z = logf(z);
-  float l = R.p != 0.0f ? R.p * ((R.s - m) * inv_t - log_z) : 0.0f;
+  float l = R.p != 0.0f ? R.p * (R.s - m) : 0.0f;
   for (int j = lane + 32; j < A.k; j += 32)
-    if (probs[j] != 0.0f) l += probs[j] * ((elem_to_f<T>(s[ids[j]]) - m) * inv_t - log_z);
+    if (probs[j] != 0.0f) l += probs[j] * (elem_to_f<T>(s[ids[j]]) - m);
   l = warp_sum(l);
-  if (lane == 0) A.loss[i] = R.some ? A.temperature * A.temperature * (R.plogp - l) : 0.0f;
+  const float t = A.temperature;
+  if (lane == 0) A.loss[i] = R.some ? fmaf(-t, l, t * t * (R.plogp + logf(z))) : 0.0f;
 }
 
 // The gradient of the kept classes in [lo, hi), which the row's pass wrote as q

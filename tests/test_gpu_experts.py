@@ -420,6 +420,34 @@ def test_distill_masks_and_extremes(torch, e):
     assert abs(loss[4].item() - want) <= 20 * U * (np.log(e) + 2) + (e / 32 + 16) * U
 
 
+@pytest.mark.parametrize("e", [40, 4096, 20001, 300000])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [0.125, 0.5, 1.0])
+def test_distill_classes_kept_by_the_teacher_and_masked_by_the_student(torch, e, dtype, T):
+    """The student's lowest value at a class that the teacher keeps: T^2 p (log p - log q) is T p |lowest| and some,
+    finite although lowest / T may not be. The gap, its product with p, the sum of at most 3 and the product with T:
+    6u of it; p within 2u (2 * 2 + k + 4), as in _distill_bounds with logits of at most 1 / T; the rest of the loss
+    is below half a step of it in fp32 and bf16 and has the bound of T^2 (log e + 2) (e / 32 + 64) u in fp16."""
+    import neural_radiance_field_b200 as nb
+    low = torch.finfo(_t(torch, dtype)).min
+    s = torch.zeros(4, e, device="cuda", dtype=_t(torch, dtype))
+    s[:, 5] = 2.0
+    s[:, 1] = low
+    s[1, 7:] = low
+    ids = torch.tensor([[1, -1, -1], [1, 5, -1], [2, 1, 5], [0, 5, 3]], device="cuda", dtype=torch.int32)
+    tl = torch.tensor([[1.0, 0, 0], [0.5, 1, 0], [0, 1, 0.25], [0, 1, 0.5]], device="cuda")
+    shifted = torch.empty(4 * e + 1, device="cuda", dtype=s.dtype)[1:].view(4, e)      # gradient aligned unlike the student
+    for grad in (None, torch.empty_like(s), shifted):
+        loss = torch.empty(4, device="cuda")
+        nb.nerf_distill_topk(s, tl, ids, T, loss, grad)
+        ref, r_grad = E.distill(_np(s), _np(tl), ids.cpu().numpy(), T)
+        assert np.isfinite(ref.astype(np.float32)).all()
+        bound = ref * U * (6 + 2 * (6 / T + 4) + 7) + T * T * (np.log(e) + 2 + 4 / T) * (e / 32 + 64) * U
+        _near(_np(loss), ref, bound, "loss")
+        if grad is not None:
+            assert torch.isfinite(grad).all() and grad[0, 1] == -T and abs(r_grad[0, 1] + T) < 1e-9
+
+
 @pytest.mark.parametrize("e,dtype", [(5003, "fp32"), (20001, "fp32"), (60000, "bf16"), (100003, "fp32")])
 def test_distill_rows_of_one_call_are_those_of_calls_of_their_own(torch, e, dtype):
     """A CTA, and clusters of two, four and eight, that take several rows one after another: each row's loss and
