@@ -22,6 +22,39 @@ namespace {
 
 constexpr int RT = 256;
 
+// A lane's dot products are summed in runs of RUN terms and the runs' sums in order: a
+// chain of 2^17 roundings, a lane's share of the widest row, was off by 7e-4 where
+// equal terms round one way. The sums of the runs wait in shared memory.
+constexpr int RUN = 512;
+template <int KC>
+struct Runs {
+  float sum[KC][RT];
+  // `done` vectors of the row lie behind the lanes, `run` make a run
+  __device__ __forceinline__ void next(float* dot, int done, int run) {
+    if (done == 0 || (done & (run - 1)) != 0) return;
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      sum[j][threadIdx.x] = done == run ? dot[j] : sum[j][threadIdx.x] + dot[j];
+      dot[j] = 0.0f;
+    }
+  }
+  // behind the last of the row's `nv` vectors
+  __device__ __forceinline__ void end(float* dot, int lane, int nv, int run) {
+    if (lane + run < nv)
+#pragma unroll
+      for (int j = 0; j < KC; ++j) dot[j] += sum[j][threadIdx.x];
+  }
+};
+template <>
+struct Runs<0> {                             // one run
+  __device__ __forceinline__ void next(float*, int, int) {}
+  __device__ __forceinline__ void end(float*, int, int, int) {}
+};
+// What a kernel does about the weights' gradients. Rows of one run (up to 4,096
+// elements on eight lanes) have a form of their own: with the runs' code the other
+// takes up to 127 registers for 80.
+enum Dots { NO_DOTS, ONE_RUN, MANY_RUNS };
+
 // a chunk of at most KC of a point's pairs: sorted rows (-1: none) and weights
 template <int KC>
 struct Pairs {
@@ -74,12 +107,14 @@ __device__ __forceinline__ void store_dots(float* dot, int G, int lane, bool on,
   }
 }
 
-template <typename T, int BYTES, int KC, bool DW>
+template <typename T, int BYTES, int KC, Dots DOTS>
 __global__ void __launch_bounds__(RT)
 rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_t n, int nv, int G,
                     const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
                     T* __restrict__ rows, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
+  constexpr bool DW = DOTS != NO_DOTS;
+  __shared__ Runs<DOTS == MANY_RUNS ? KC : 0> runs;
   constexpr int U = 4;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
@@ -90,6 +125,7 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
     float dot[KC] = {};
     if (on)
       for (int v0 = lane; v0 < nv; v0 += U * G) {
+        runs.next(dot, v0 - lane, RUN / V::N * G);
         V a[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -127,16 +163,19 @@ rows_scatter_kernel(const T* __restrict__ x, const T* __restrict__ other, int64_
           }
         }
       }
+    if (on) runs.end(dot, lane, nv, RUN / V::N * G);
     if (DW) store_dots<KC>(dot, G, lane, on, i, k, j0, dw);
   }
 }
 
-template <typename T, int BYTES, int KC, bool DW>
+template <typename T, int BYTES, int KC, Dots DOTS>
 __global__ void __launch_bounds__(RT)
 rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t n, int nv, int G,
                    const int32_t* __restrict__ pos, int k, const float* __restrict__ weights,
                    T* __restrict__ out, float* __restrict__ dw) {
   using V = Vec<T, BYTES>;
+  constexpr bool DW = DOTS != NO_DOTS;
+  __shared__ Runs<DOTS == MANY_RUNS ? KC : 0> runs;
   constexpr int U = KC == 2 || BYTES <= 4 ? 4 : KC == 4 ? 2 : 1;                  // vectors of a row that a lane has in flight
   const int lane = threadIdx.x & (G - 1);
   const int64_t i = (int64_t)blockIdx.x * (RT / G) + threadIdx.x / G, m = n * k;
@@ -147,6 +186,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
     float dot[KC] = {};
     if (on)
       for (int v0 = lane; v0 < nv; v0 += U * G) {
+        runs.next(dot, v0 - lane, RUN / V::N * G);
         V a[U], b[U][KC];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -177,6 +217,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
             }
           }
       }
+    if (on) runs.end(dot, lane, nv, RUN / V::N * G);
     if (DW) store_dots<KC>(dot, G, lane, on, i, k, 0, dw);
     return;
   }
@@ -206,6 +247,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
       float dot[KC] = {};
       if (on)
         for (int v = lane; v < nv; v += G) {
+          runs.next(dot, v - lane, RUN / V::N * G);
           V a;
           a.load(x, i * nv + v);
 #pragma unroll
@@ -217,6 +259,7 @@ rows_gather_kernel(const T* __restrict__ rows, const T* __restrict__ x, int64_t 
             for (int c = 0; c < V::N; ++c) dot[j] = fmaf(a.get(c), b.get(c), dot[j]);
           }
         }
+      if (on) runs.end(dot, lane, nv, RUN / V::N * G);
       store_dots<KC>(dot, G, lane, on, i, k, j0, dw);
     }
 }
@@ -233,14 +276,14 @@ struct RowArgs {
   cudaStream_t st;
 };
 
-template <bool SCATTER, typename T, int BYTES, int KC, bool DW>
+template <bool SCATTER, typename T, int BYTES, int KC, Dots DOTS>
 void run(const RowArgs& A) {
   const unsigned grid = (unsigned)((A.n + RT / A.G - 1) / (RT / A.G));
   if (SCATTER)
-    rows_scatter_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
+    rows_scatter_kernel<T, BYTES, KC, DOTS><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
                                                                  A.k, A.w, (T*)A.out, A.dw);
   else
-    rows_gather_kernel<T, BYTES, KC, DW><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
+    rows_gather_kernel<T, BYTES, KC, DOTS><<<grid, RT, 0, A.st>>>((const T*)A.a, (const T*)A.b, A.n, A.nv, A.G, A.pos,
                                                                 A.k, A.w, (T*)A.out, A.dw);
 }
 // Pairs in chunks of two for k <= 2, of four for k <= 4, else of eight: an unused
@@ -248,11 +291,17 @@ void run(const RowArgs& A) {
 // dispatch / combine / combine's backward: k 2 in chunks of two 49 / 46 / 78 us, of
 // four 49 / 54 / 84, of eight 51 / 120 / 86; k 4 of four 83 / 75 / 146, of eight
 // 83 / 131 / 148.
-template <bool SCATTER, typename T, int BYTES>
+template <bool SCATTER, typename T, int BYTES, Dots DOTS>
 void run_k(const RowArgs& A) {
-  if (A.k <= 2) A.dw ? run<SCATTER, T, BYTES, 2, true>(A) : run<SCATTER, T, BYTES, 2, false>(A);
-  else if (A.k <= 4) A.dw ? run<SCATTER, T, BYTES, 4, true>(A) : run<SCATTER, T, BYTES, 4, false>(A);
-  else A.dw ? run<SCATTER, T, BYTES, 8, true>(A) : run<SCATTER, T, BYTES, 8, false>(A);
+  if (A.k <= 2) run<SCATTER, T, BYTES, 2, DOTS>(A);
+  else if (A.k <= 4) run<SCATTER, T, BYTES, 4, DOTS>(A);
+  else run<SCATTER, T, BYTES, 8, DOTS>(A);
+}
+template <bool SCATTER, typename T, int BYTES>
+void run_dots(const RowArgs& A) {
+  if (!A.dw) run_k<SCATTER, T, BYTES, NO_DOTS>(A);
+  else if (A.nv <= RUN / Vec<T, BYTES>::N * A.G) run_k<SCATTER, T, BYTES, ONE_RUN>(A);
+  else run_k<SCATTER, T, BYTES, MANY_RUNS>(A);
 }
 template <bool SCATTER, typename T>
 cudaError_t run_t(RowArgs A, int width) {
@@ -266,10 +315,10 @@ cudaError_t run_t(RowArgs A, int width) {
   const int widest = bytes >= 8 && A.nv <= 16 ? 4 : 8, lanes = bytes >= 8 ? A.nv : (A.nv + 3) / 4;
   A.G = 1;
   while (A.G < lanes && A.G < widest) A.G *= 2;
-  if (bytes == 16) run_k<SCATTER, T, 16>(A);
-  else if (bytes == 8) run_k<SCATTER, T, 8>(A);
-  else if (bytes == 4) run_k<SCATTER, T, 4>(A);
-  else run_k<SCATTER, T, (int)sizeof(T)>(A);
+  if (bytes == 16) run_dots<SCATTER, T, 16>(A);
+  else if (bytes == 8) run_dots<SCATTER, T, 8>(A);
+  else if (bytes == 4) run_dots<SCATTER, T, 4>(A);
+  else run_dots<SCATTER, T, (int)sizeof(T)>(A);
   return cudaGetLastError();
 }
 template <bool SCATTER>

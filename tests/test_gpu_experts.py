@@ -247,6 +247,36 @@ def test_rows(torch, n, k, e, width, dtype, weighted, shift):
     assert torch.equal(d_x2, d_x)
 
 
+@pytest.mark.parametrize("k", [1, 3, 8, 12])
+@pytest.mark.parametrize("width,shift", [(1 << 20, 0), (1 << 20, 1), (70001, 0), (4096, 0), (4100, 0), (8191, 1), (8224, 0)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_gradients_of_wide_rows(torch, width, shift, k, dtype):
+    """Equal terms, whose roundings all go one way, and terms of one sign: eight lanes sum runs of 512 terms, then the
+    runs in order, then each other, so no sum has more than 512 + width / 4096 + 4 roundings."""
+    import neural_radiance_field_b200 as nb
+    gen = torch.Generator(device="cuda").manual_seed(width + k)
+    n, t = 2, _t(torch, dtype)
+
+    def make(m):
+        flat = torch.rand(m * width + shift, device="cuda", generator=gen).to(t)
+        flat[:m * width // 2] = 0.1
+        return flat[shift:].view(m, width)
+
+    x, rows, d_x = make(n), make(n * k), make(n)
+    pos = torch.randperm(n * k, device="cuda", generator=gen).int().view(n, k)
+    pos[1, k - 1] = -1
+    dw, dw2 = torch.full((n, k), 7.0, device="cuda"), torch.full((n, k), 7.0, device="cuda")
+    nb.nerf_expert_dispatch_backward(rows, x, pos, d_x, None, dw)
+    ref = E.dots(_np(rows), _np(x), pos.cpu().numpy())
+    bound = (512 + width / 4096 + 4) * U * ref
+    _near(_np(dw), ref, bound, "dispatch")
+    nb.nerf_expert_combine_backward(x, rows, pos, torch.empty(n * k * width + shift, device="cuda", dtype=t)[shift:].view(n * k, width), None, dw2)
+    _near(_np(dw2), ref, bound, "combine")
+    out = torch.empty_like(d_x) if shift == 0 else make(n)
+    nb.nerf_expert_combine(rows, pos, out)
+    assert torch.equal(out, d_x)                         # the sum does not depend on whether d_weights is asked for
+
+
 def test_rows_nonfinite(torch):
     """An infinity or NaN in a kept row reaches its own point only; in rows that nothing names it reaches none."""
     import neural_radiance_field_b200 as nb
