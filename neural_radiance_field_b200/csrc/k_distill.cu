@@ -163,12 +163,12 @@ template <typename T>
 __device__ __forceinline__ void write_loss(const DistillArgs& A, int64_t i, const T* s, float m, float z,
                                            const float* probs, const int32_t* ids, const Teacher& R) {
   const int lane = threadIdx.x & 31;
+  const float t = A.temperature, rest = R.some ? t * t * (R.plogp + logf(z)) : 0.0f;
   float l = R.p != 0.0f ? R.p * (R.s - m) : 0.0f;
   for (int j = lane + 32; j < A.k; j += 32)
     if (probs[j] != 0.0f) l += probs[j] * (elem_to_f<T>(s[ids[j]]) - m);
   l = warp_sum(l);
-  const float t = A.temperature;
-  if (lane == 0) A.loss[i] = R.some ? fmaf(-t, l, t * t * (R.plogp + logf(z))) : 0.0f;
+  if (lane == 0) A.loss[i] = fmaf(-t, l, rest);   // nothing kept: both are 0
 }
 
 // The gradient of the kept classes in [lo, hi), which the row's pass wrote as q
