@@ -460,8 +460,10 @@ NERF_API nerf_status nerf_expert_combine_backward(const void* d_out, const void*
  * `dtype`, row_scale [n] fp32 (NULL: 1). An entry is kept when its id is in
  * 0..n_classes-1 and its logit is not -inf; a row that keeps none has loss 0
  * and gradient 0. An id given twice counts twice. A student logit of -inf has
- * q = 0 (a row of nothing else has no distribution: NaN). 1 <= k <= 256,
- * 1 <= n_classes <= 2^30, 2^-60 <= T <= 2^60. */
+ * q = 0 (a row of nothing else has no distribution: NaN). The loss is the
+ * difference of two sums of about T^2 log(n_classes): where p and q nearly agree
+ * (all classes kept, T large) its absolute error stays theirs, some 2^-22 of them.
+ * 1 <= k <= 256, 1 <= n_classes <= 2^30, 2^-60 <= T <= 2^60. */
 NERF_API nerf_status nerf_distill_topk(const void* student, int dtype, int64_t n, int n_classes,
                                        const float* teacher_logits, const int32_t* teacher_ids,
                                        int k, float temperature, const float* row_scale,
@@ -488,7 +490,7 @@ NERF_API nerf_status nerf_cells_backward_workspace(int64_t n_rows, int n_cells,
 
 /* Weight gradient of nerf_cells_forward: x, d, offset, cell_w as in the forward
  * pass, hidden [n_rows][64] as it wrote them (the hidden layers decide the ReLU
- * masks, the derivative at 0 taken as 0), d_raw [n_rows][4]. grad_cell_w
+ * masks, the derivative at 0 and at NaN taken as 0), d_raw [n_rows][4]. grad_cell_w
  * [n_cells][3317] is overwritten (0 for a cell without rows). Sums run in a
  * fixed order: the result does not vary between runs. workspace as in
  * nerf_expert_sort. */

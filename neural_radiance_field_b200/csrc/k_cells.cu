@@ -20,16 +20,18 @@
 // operations in place of a second evaluation. With base q = 0..14
 // (coordinate q / 5, octave 2 (q % 5)), base 15 stands for x, y, z and a constant.
 //
-// Why not tcgen05: its operands come from shared memory, so every layer's inputs
-// would be split and written there (768 bytes a row forward) behind barriers, as
-// kilo_eval_kernel does for the renderer; at N = 32 that costs more than the
-// products. mma.sync runs at 0.9 TMAC/s an SM in tf32 (measured), 57 us for the
-// forward layers of 786,432 rows. With 786,432 rows over 4,096 cells (2,702 of
-// them with rows) the forward pass with its hidden layers takes 140 us (2.0 TB/s
-// of 287 MB, 0.31 of the copy rate; tensor pipe 44 % busy, issue slots 50 %, shared
-// memory 52 %), the weight gradient 195 us (tensor pipe 45 %, issue slots 56 %,
-// shared memory 52 %): no unit is full, both are bound by each warp's chain of
-// encoding, split and product at the 16 or 12 warps that an SM's registers hold.
+// mma.sync and not tcgen05: with operands in shared memory every layer's inputs would
+// be split and written there (768 bytes a row forward) behind barriers, as
+// kilo_eval_kernel does for the renderer. Operand A can also come from tensor memory,
+// to which a thread that owns a row could write its split activations; that form has
+// not been built. mma.sync runs at 0.9 TMAC/s an SM in tf32 (measured), 57 us for the
+// forward layers of 786,432 rows: a floor of the instruction, not of the card. With
+// 786,432 rows over 4,096 cells (2,702 of them with rows) the forward pass with its
+// hidden layers takes 137 us on the device (2.1 TB/s of 287 MB, 0.32 of the copy rate;
+// tensor pipe 44 % busy, issue slots 52 %, shared memory 52 %), the weight gradient
+// 193 us (tensor pipe 45 %, issue slots 56 %, shared memory 51 %): no unit is full,
+// both are bound by each warp's chain of encoding, split and product at the 16 or 12
+// warps that an SM's registers hold.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
@@ -195,10 +197,10 @@ constexpr int CF_WARPS = 4, CF_THREADS = CF_WARPS * 32;
 constexpr int CF_ROWS = CF_WARPS * 32;       // rows of a tile, 32 per warp
 constexpr int CF_PER_SM = 4;
 // A tile of up to CF_SPREAD rows is shared by all four warps, 16 rows each, else a
-// warp takes 32: with few rows to a cell the tile's time is one warp's chain. 20,000
-// rows of 4,096 cells take 34 us (40 without; 36 with 32 rows, 8 to a warp), 70,000
-// 41 us (46; 50), the 192 rows of a ray 11.3 us (12.7). A row's operations and their
-// order are the same.
+// warp takes 32: with few rows to a cell the tile's time is one warp's chain. On the
+// device 20,000 rows of 4,096 cells take 34 us (39 without; 36 with 32 rows, 8 to a
+// warp), 70,000 41 us (45; 50), 2,000 22.7 (26.2; 22.3), the 192 rows of a ray 9.2 us
+// (10.6; 9.5). A row's operations and their order are the same.
 constexpr int CF_SPREAD = 64;
 // rows of each warp in a tile with `rows` rows left
 __device__ __forceinline__ int share_of(int64_t rows) { return rows <= CF_SPREAD ? CF_SPREAD / CF_WARPS : CF_ROWS / CF_WARPS; }
@@ -227,7 +229,10 @@ __device__ __forceinline__ float4 b_fragment(float b0, float b1) {
 // 2t + 1 of the four tiles, has features 8t .. 8t + 7: a run that it stores at once.
 __device__ __forceinline__ int out_feature(int j, int n) { return 8 * (n >> 1) + 2 * j + (n & 1); }
 // One k step of a layer: M fragments of 16 rows x 32 outputs (four). The three
-// products of an accumulator are 4 M instructions apart.
+// products of an accumulator are 4 M instructions apart. The tensor core truncates when
+// it adds to the accumulator: the hidden layers are within 5.3e-7 of their norm. Sums
+// of every step, or of every two, added by rounded additions bring that to 1.2e-7 or
+// 1.7e-7 (fp32 products: 1.5e-7), at 150 or 143 us for the batch in place of 137.
 template <int M>
 __device__ __forceinline__ void layer_step(float (&c)[M][4][4], const uint32_t (&ah)[M][4],
                                            const uint32_t (&al)[M][4], const float4* w) {

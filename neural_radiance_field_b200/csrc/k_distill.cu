@@ -18,10 +18,11 @@
 // row's 16-byte vectors start wherever its address allows; up to 14 elements
 // before and after them go one by one.
 //
-// 65,536 rows of 4,096 bf16 with gradient: 207 us, 5.2 TB/s (0.81 of the measured
-// copy rate; two exponentials an element keep the XU pipe 63 % busy). 777 rows of
-// 100,003 fp32: 152 us, 4.1 TB/s (0.64): 33 clusters of eight fit the GPCs, 264 of
-// 296 CTAs, and each row ends in a cluster barrier.
+// 65,536 rows of 4,096 bf16 with gradient: 203 us on the device (212 to 216 call by
+// call), 5.3 TB/s (0.83 of the measured copy rate; two exponentials an element keep the
+// XU pipe 62 % busy). 777 rows of 100,003 fp32: 149 us (152 call by call), 4.2 TB/s
+// (0.65): 33 clusters of eight fit the GPCs, 264 of 296 CTAs, and each row ends in a
+// cluster barrier.
 #include <cooperative_groups.h>
 
 #include "nerf_experts.cuh"
@@ -570,7 +571,7 @@ cudaError_t run_clusters(K kernel, int64_t teams, int threads, size_t smem, int 
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
   cfg.gridDim = dim3((unsigned)(teams * C));
-  if (C > 1 && teams * C > 148) {
+  if (C > 1 && teams * C > 148) {            // fewer run at once in any case, and asking takes the host 0.3 us a call
     int most = 0;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
     if (e != cudaSuccess) return e;
@@ -623,6 +624,9 @@ cudaError_t run_t(const DistillArgs& A, cudaStream_t st) {
   const int64_t bytes = (int64_t)A.classes * sizeof(T);
   // the vectors of student and gradient rows coincide when both start alike
   if (A.grad && ((uintptr_t)A.grad - (uintptr_t)A.student) % 16) return run_wide<T, (int)sizeof(T)>(A, st);
+  // Vectors of a lane, as few as hold the row: 65,536 rows of 512 bytes 43 us with one,
+  // 45 with two; of 1 KB 47 with two, 61 with eight; of 4 KB 91 with eight, 111 with
+  // sixteen (100 such rows 4.3 us, as CTAs of their own 4.0; 592 rows 4.4, 4.5).
   if (bytes <= 512) return run_rows<T, 1>(A, st);
   if (bytes <= 1024) return run_rows<T, 2>(A, st);
   if (bytes <= 4096) return run_rows<T, 8>(A, st);

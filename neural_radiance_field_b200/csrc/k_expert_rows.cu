@@ -10,10 +10,12 @@
 // lanes, which take several vectors of a wide row at once: that keeps more loads
 // in flight and spreads the pairs' index work over them. Rows move in vectors of
 // 16, 8 or 4 bytes, the widest that their size and the buffers allow, else by
-// element. 262,144 points of 256 bf16 with two pairs each: dispatch 65 us (6.0
-// TB/s, 0.93 of the measured copy rate), combine's backward with its weight
-// gradient 102 us (0.98); 786,432 points of 4 fp32 with eight pairs: combine 33 us
-// (0.73; its pairs' positions and weights are a third of the bytes).
+// element. On the device, 262,144 points of 256 bf16 with two pairs each: dispatch
+// 62 us (6.2 TB/s, 0.96 of the measured copy rate), combine's backward with its weight
+// gradient 100 us (0.99); 786,432 points of 4 fp32 with eight pairs: combine 30 us
+// (0.79; its pairs' positions and weights are a third of the bytes). The grid covers
+// points: few points with wide rows leave most of the GPU idle (300 points of 131,072
+// fp32 with three pairs: 2.0 ms of 0.12).
 #include "nerf_experts.cuh"
 #include "nerf_vec.cuh"
 

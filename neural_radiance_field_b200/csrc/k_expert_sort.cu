@@ -22,10 +22,11 @@
 //            whatever the timing.
 // The launches overlap: place counts its first tile while columns still runs.
 //
-// 6.3 M pairs over 4,096 experts, eight neighbouring cells a point: 52 us, 1.4 TB/s of
-// the 75 MB that the sort has to read and write (0.22 of the copy rate); uniform
-// ids: 38 us. Count takes 10 us, columns 5; place is bound by its chains through
-// shared memory (counter, add, counter) at the 16 warps whose counters fit an SM.
+// 6.3 M pairs over 4,096 experts, eight neighbouring cells a point: 52 us on the device
+// (55 call by call), 1.4 TB/s of the 75 MB that the sort has to read and write (0.22 of
+// the copy rate); uniform ids: 37 us. Count takes 10 us, columns 5; place is bound by
+// its chains through shared memory (counter, add, counter) at 16 warps an SM. The
+// counters of 24 would fit (213 KB at 4,096 experts); that has not been tried.
 #include "nerf_experts.cuh"
 
 namespace nerfb {
@@ -60,8 +61,11 @@ struct SortPlan {
   int ctas;
   int64_t chunk;                             // pairs of a CTA, a multiple of ES_T
 };
-// Small tables leave room for two CTAs to an SM (6.3 M pairs of 1,000 experts take
-// 75 us, with one 120; of 64 experts 66 and 64).
+// Small tables leave room for two CTAs to an SM. 6.3 M pairs of a gate, two and one: 64
+// experts 65 and 65 us (uniform ids 51 and 53), 256: 63 and 83, 1,000: 66 and 84, 1,024:
+// 66 and 84; only 100,000 points with two of 64 experts are quicker with one, 11.0 and
+// 9.4. (The tables of up to 3,100 experts would fit twice as well: 2,048 experts take
+// 88 us here, 68 with two.)
 SortPlan sort_plan(int64_t pairs, int n_experts) {
   const int64_t most = n_experts <= 1024 ? ES_MOST_CTAS : 148, want = (pairs + ES_CHUNK - 1) / ES_CHUNK;
   const int64_t ctas = want < most ? want : most;
