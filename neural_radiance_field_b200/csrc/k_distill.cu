@@ -571,7 +571,7 @@ cudaError_t run_clusters(K kernel, int64_t teams, int threads, size_t smem, int 
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
   cfg.gridDim = dim3((unsigned)(teams * C));
-  if (C > 1 && teams * C > 148) {            // fewer run at once in any case, and asking takes the host 0.3 us a call
+  if (C > 1 && teams * C > 148) {            // so few all run at once, and asking takes the host 0.3 us
     int most = 0;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
     if (e != cudaSuccess) return e;

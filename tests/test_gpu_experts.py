@@ -720,12 +720,14 @@ def test_cells_that_are_not_finite_show_it(torch, rows, bad):
     mine = torch.zeros(len(x), device="cuda", dtype=torch.bool)
     mine[rows:2 * rows + 3] = True
     f = 9                                                # the feature whose weight is not finite
-    for at, layer in ((f * 63 + 20, 1), (2016 + f, 1), (2048 + f * 32 + 3, 2), (3072 + f, 2)):   # W1, b1, W2, b2
+    b1 = 32 * 63 + f
+    b2 = 32 * 63 + 32 + 32 * 32 + f
+    for at, layer in ((f * 63 + 20, 1), (b1, 1), (32 * 63 + 32 + f * 32 + 3, 2), (b2, 2)):   # W1, b1, W2, b2
         w2 = w.copy()
         w2[1, at] = bad
         raw2, hid2 = _cells_once(torch, x, d, off, w2)
         assert same(raw, raw2, ~mine) and same(hid, hid2, ~mine)
-        if at in (2016 + f, 3072 + f) and bad == -np.inf:    # a bias of -inf turns its feature off
+        if at in (b1, b2) and bad == -np.inf:    # a bias of -inf turns its feature off
             off1 = hid2[mine, 32 * (layer - 1) + f]
             assert off1.eq(0).all()
             continue
